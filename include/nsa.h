@@ -374,6 +374,128 @@ nsa_status_t nsa_dsa_prefill(const void* q, const void* k, const void* v, const 
                              const nsa_heads_t* heads, void* out, int32_t* idx_out, float* score_out,
                              void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- Full-attention layers ----
+ * Models that use NSA or DSA layers keep full (dense) attention in some layers
+ * ("Native Sparse Attention" lesson, introduction: the baseline that NSA replaces),
+ * and every layer, sparse or full, takes queries and keys that were normalised and
+ * rotated. The entry points below cover both; they share the head geometry, the
+ * packed prompts, the caches and the pages of the NSA entry points. */
+enum {
+  NSA_OP_FULL_PREFILL = 6,
+  NSA_OP_FULL_BACKWARD = 7,
+  NSA_OP_TREE_DECODE = 8,
+  NSA_OP_ROPE_BACKWARD = 9
+};
+#define NSA_MAX_NODES 64
+
+/* Workspace bytes of the calls below. batch, total_tokens, max_len as in
+ * nsa_workspace_size (NSA_OP_ROPE_BACKWARD reads total_tokens only); max_nodes =
+ * node slots per sequence (NSA_OP_TREE_DECODE, 1 .. NSA_MAX_NODES; not read by the
+ * others). 0 for invalid arguments. */
+size_t nsa_full_workspace_size(int op, const nsa_heads_t* heads, int32_t batch, int64_t total_tokens,
+                               int32_t max_len, int32_t max_nodes);
+
+/* Rotary position: the first d_rot channels of a head turn (d_rot a multiple of
+ * 16, 0 .. d_k). interleaved != 0: pairs (2i, 2i + 1); 0: pairs (i, i + d_rot/2).
+ * eps: added to the mean square of the norm (> 0). */
+typedef struct {
+  int32_t d_rot, interleaved;
+  float eps;
+} nsa_rope_params_t;
+
+/* Queries and keys ready for attention: RMS norm of each head with a weight, then
+ * the rotary position, in one pass over the projections:
+ *   y = x * rsqrt(mean(x^2) + eps) * w
+ *   (a, b) -> (a cos - b sin, a sin + b cos), angle positions[n] * inv_freq[i]
+ * (angle in fp64, the rest in fp32, rounded to bf16 once).
+ *   q         bf16, token n at q + n * q_stride elements: [H_q, d_k] packed
+ *   k, v      likewise with k_stride [H_kv, d_k] and v_stride [H_kv, d_v]; the
+ *             strides are multiples of 8 (views of one fused projection serve).
+ *             v may be NULL (with v_out): values are not copied
+ *   w_q, w_k  fp32 [d_k];  inv_freq fp32 [d_rot / 2] (not read when d_rot = 0)
+ *   positions DEVICE int32 [N], any value
+ *   cache_rows DEVICE int64 [N] or NULL: row of k_out / v_out that token n is
+ *             written to (row n when NULL). A token whose row is outside
+ *             [0, n_rows) writes neither key nor value (padding: -1); rows must
+ *             differ. Rows that no token names are left as they were.
+ *             A paged cache's row is page * page_size + offset.
+ *   n_rows    rows of k_out and v_out (>= N when cache_rows is NULL)
+ *   q_out     bf16 out [N, H_q, d_k]; may be q when q is packed
+ *   k_out     bf16 out [n_rows, H_kv, d_k]; may be k when packed and cache_rows is NULL
+ *   v_out     bf16 out [n_rows, H_kv, d_v] or NULL
+ * N = 0 launches nothing. No workspace. */
+nsa_status_t nsa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, const float* w_q, const float* w_k, const float* inv_freq,
+                              const int32_t* positions, const int64_t* cache_rows, int64_t n_rows, int64_t N,
+                              const nsa_heads_t* heads, const nsa_rope_params_t* rope, void* q_out, void* k_out,
+                              void* v_out, void* stream);
+
+/* Backward of nsa_qk_norm_rope (its inputs, without cache rows):
+ *   dq_out, dk_out  bf16 [N, H_q, d_k], [N, H_kv, d_k]: gradients of q_out, k_out
+ *   dq, dk    bf16 out, token n at dq + n * dq_stride (dk_stride) elements:
+ *             gradients of q, k
+ *   dw_q, dw_k fp32 out [d_k]: summed over tokens and heads in a fixed order
+ * dq may be dq_out and dk may be dk_out (packed). Workspace:
+ * nsa_full_workspace_size(NSA_OP_ROPE_BACKWARD, heads, 1, N, 0, 0). */
+nsa_status_t nsa_qk_norm_rope_backward(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                       const float* w_q, const float* w_k, const float* inv_freq,
+                                       const int32_t* positions, int64_t N, const void* dq_out, const void* dk_out,
+                                       const nsa_heads_t* heads, const nsa_rope_params_t* rope, void* dq,
+                                       int64_t dq_stride, void* dk, int64_t dk_stride, float* dw_q, float* dw_k,
+                                       void* workspace, size_t ws_bytes, void* stream);
+
+/* Causal full attention over packed prompts: token t of a sequence attends to
+ * its tokens 0 .. t.
+ *   q, k, v, cu_seqlens (HOST), batch, heads: as in nsa_prefill
+ *   scale     softmax scale, 0 means 1/sqrt(d_k)
+ *   out       bf16 out [N, H_q, d_v]
+ *   lse_out   fp32 out or NULL [N, H_q]: log of the softmax denominator (natural),
+ *             which nsa_full_prefill_backward takes
+ * Rows past cu_seqlens[batch] are neither read into a result nor written; NaN or
+ * infinity in one sequence does not reach another. Within a sequence a value that
+ * is not finite may reach queries up to 127 tokens before it. Workspace:
+ * nsa_full_workspace_size(NSA_OP_FULL_PREFILL, heads, batch, N, max_len, 0). */
+nsa_status_t nsa_full_prefill(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int32_t batch,
+                              const nsa_heads_t* heads, float scale, void* out, float* lse_out, void* workspace,
+                              size_t ws_bytes, void* stream);
+
+/* Full attention of drafted tokens over a cache that already holds them
+ * (speculative decoding). Sequence b has cache_lens[b] tokens in the cache, of
+ * which the last n_nodes[b] are the nodes of a tree of drafts, node i in cache row
+ * cache_lens[b] - n_nodes[b] + i; its query attends to every token before the
+ * nodes and to the nodes its mask names. One node is the single-token decode.
+ *   q         bf16 [batch, max_nodes, H_q, d_k]
+ *   k_cache   bf16 [batch, Lmax, H_kv, d_k]; v_cache with d_v
+ *   cache_lens DEVICE int32 [batch], n_nodes[b] <= cache_lens[b] <= max_len
+ *   n_nodes   DEVICE int32 [batch], 0 .. max_nodes, or NULL (max_nodes each)
+ *   tree_mask DEVICE uint64 [batch, max_nodes]: bit j of word i set when node i
+ *             sees node j (its ancestors and itself; bits from n_nodes[b] on are
+ *             not read), or NULL: a chain, node i sees nodes 0 .. i
+ *   max_nodes 1 .. NSA_MAX_NODES;  scale 0 means 1/sqrt(d_k)
+ *   out       bf16 out [batch, max_nodes, H_q, d_v]; lse_out fp32 out or NULL
+ *             [batch, max_nodes, H_q]
+ * Rows of nodes from n_nodes[b] on are left as they were (n_nodes[b] = 0: the
+ * whole sequence). A node that sees nothing gets zeros and lse -infinity. Lengths
+ * out of range are recorded in the status word and the sequence is skipped. Cache
+ * rows from cache_lens[b] on are not read into a result. Workspace:
+ * nsa_full_workspace_size(NSA_OP_TREE_DECODE, heads, batch, 0, max_len, max_nodes). */
+nsa_status_t nsa_full_tree_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* cache_lens,
+                                  const int32_t* n_nodes, const uint64_t* tree_mask, int32_t batch,
+                                  int32_t max_nodes, int32_t Lmax, int32_t max_len, const nsa_heads_t* heads,
+                                  float scale, void* out, float* lse_out, void* workspace, size_t ws_bytes,
+                                  void* stream);
+
+/* The same over a paged cache: pools and block_table as in nsa_decode_paged
+ * (page_size a multiple of 64; only pages that a length reaches are read; page ids
+ * outside [0, n_pages) are recorded in the status word and read as page 0);
+ * max_len <= max_pages * page_size. */
+nsa_status_t nsa_full_tree_decode_paged(const void* q, const void* k_pool, const void* v_pool, int32_t n_pages,
+                                        int32_t page_size, const int32_t* block_table, int32_t max_pages,
+                                        const int32_t* cache_lens, const int32_t* n_nodes, const uint64_t* tree_mask,
+                                        int32_t batch, int32_t max_nodes, int32_t max_len, const nsa_heads_t* heads,
+                                        float scale, void* out, float* lse_out, void* workspace, size_t ws_bytes,
+                                        void* stream);
+
 /* Opt-in per-kernel timing (no compute change). While enabled, every entry point
  * records a CUDA event pair on its stream around each of its kernel launches.
  * nsa_profile_read() waits for the recorded events, writes for each of the
@@ -381,7 +503,7 @@ nsa_status_t nsa_dsa_prefill(const void* q, const void* k, const void* v, const 
  * the previous read, and resets them. Slot names: nsa_profile_slot_name(). The
  * events are created on first use and reused; this is the only state the
  * library keeps between calls. Returns NSA_ERR_CUDA if an event query fails. */
-#define NSA_PROFILE_SLOTS 12
+#define NSA_PROFILE_SLOTS 17
 nsa_status_t nsa_profile_enable(int32_t enable);
 nsa_status_t nsa_profile_read(double* ms_out, int64_t* launches_out, int32_t n_slots);
 const char* nsa_profile_slot_name(int32_t slot);

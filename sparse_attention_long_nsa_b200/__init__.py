@@ -35,9 +35,12 @@ EXPORTED = ("nsa_workspace_size", "nsa_workspace_init", "nsa_check_device_status
             "nsa_noalloc_check_status", "nsa_compress_weights_size", "nsa_compress_prepare", "nsa_compress_prepared",
             "nsa_decode_paged", "nsa_prefill_backward", "nsa_dsa_workspace_size", "nsa_dsa_decode",
             "nsa_dsa_prefill", "nsa_prefill", "nsa_decode", "nsa_profile_enable", "nsa_profile_read", "nsa_profile_slot_name",
-            "nsa_status_string", "nsa_last_error_detail")
-NSA_PROFILE_SLOTS = 12
+            "nsa_status_string", "nsa_last_error_detail", "nsa_full_workspace_size", "nsa_qk_norm_rope",
+            "nsa_qk_norm_rope_backward", "nsa_full_prefill", "nsa_full_tree_decode", "nsa_full_tree_decode_paged")
+NSA_PROFILE_SLOTS = 17
 NSA_OP_DSA_DECODE, NSA_OP_DSA_PREFILL = 4, 5
+NSA_OP_FULL_PREFILL, NSA_OP_FULL_BACKWARD, NSA_OP_TREE_DECODE, NSA_OP_ROPE_BACKWARD = 6, 7, 8, 9
+NSA_MAX_NODES = 64
 # the checking build exports one more symbol (include/nsa_check.h)
 CHECK_EXPORTED = EXPORTED + ("nsa_test_set_fault",)
 FAULT_NONE, FAULT_DECODE_FINE_TILE, FAULT_PREFILL_K_TILE = 0, 1, 2
@@ -66,6 +69,11 @@ class DsaParams(ctypes.Structure):
     """nsa_dsa_params_t"""
     _fields_ = [("H_I", ctypes.c_int32), ("d_I", ctypes.c_int32), ("top_k", ctypes.c_int32),
                 ("scale", ctypes.c_float)]
+
+
+class RopeParams(ctypes.Structure):
+    """nsa_rope_params_t"""
+    _fields_ = [("d_rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 def make_params(l_cmp=32, stride=16, l_sel=64, top_n=16, window=512, force_first=1, force_local=2,
@@ -164,6 +172,23 @@ def _load(path: str) -> ctypes.CDLL:
     L.nsa_decode.restype = ctypes.c_int
     L.nsa_decode.argtypes = [P, P, P, P, P, P, I32, I32, I32, I32, P, ctypes.POINTER(Heads),
                              ctypes.POINTER(Params), P, P, P, P, SZ, P]
+    F32 = ctypes.c_float
+    L.nsa_full_workspace_size.restype = SZ
+    L.nsa_full_workspace_size.argtypes = [ctypes.c_int, ctypes.POINTER(Heads), I32, I64, I32, I32]
+    L.nsa_qk_norm_rope.restype = ctypes.c_int
+    L.nsa_qk_norm_rope.argtypes = [P, I64, P, I64, P, I64, P, P, P, P, P, I64, I64, ctypes.POINTER(Heads),
+                                   ctypes.POINTER(RopeParams), P, P, P, P]
+    L.nsa_qk_norm_rope_backward.restype = ctypes.c_int
+    L.nsa_qk_norm_rope_backward.argtypes = [P, I64, P, I64, P, P, P, P, I64, P, P, ctypes.POINTER(Heads),
+                                            ctypes.POINTER(RopeParams), P, I64, P, I64, P, P, P, SZ, P]
+    L.nsa_full_prefill.restype = ctypes.c_int
+    L.nsa_full_prefill.argtypes = [P, P, P, P, I32, ctypes.POINTER(Heads), F32, P, P, P, SZ, P]
+    L.nsa_full_tree_decode.restype = ctypes.c_int
+    L.nsa_full_tree_decode.argtypes = [P, P, P, P, P, P, I32, I32, I32, I32, ctypes.POINTER(Heads), F32, P, P, P, SZ,
+                                       P]
+    L.nsa_full_tree_decode_paged.restype = ctypes.c_int
+    L.nsa_full_tree_decode_paged.argtypes = [P, P, P, I32, I32, P, I32, P, P, P, I32, I32, I32,
+                                             ctypes.POINTER(Heads), F32, P, P, P, SZ, P]
     L.nsa_profile_enable.restype = ctypes.c_int
     L.nsa_profile_enable.argtypes = [I32]
     L.nsa_profile_read.restype = ctypes.c_int
@@ -395,6 +420,207 @@ def nsa_dsa_prefill(q, k, v, qi, wi, ki, cu_seqlens, dp: DsaParams, heads: Heads
                                  _ptr(cu_seqlens, torch.int32, "cpu"), B, ctypes.byref(dp), ctypes.byref(heads),
                                  _ptr(out, torch.bfloat16), _ptr(idx_out, torch.int32), _ptr(score_out, torch.float32),
                                  _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "nsa_dsa_prefill")
+
+
+def _rows(t: torch.Tensor, heads: int, dim: int, name: str) -> tuple:
+    """(pointer, row stride) of bf16 rows [N, heads, dim] whose heads are packed: a
+    whole tensor or a view of a fused projection."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name}: expected [N, {heads}, {dim}], got {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != dim):
+        raise ValueError(f"{name}: the heads of a token must be packed")
+    return t.data_ptr(), s0 if t.shape[0] > 1 else max(s0, heads * dim)
+
+
+def _shape(t: Optional[torch.Tensor], shape: tuple, name: str):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+
+
+def _on(device, stream, *tensors):
+    """The stream of a call whose tensors live on `device`: the given one, or the
+    current stream of that device."""
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device} in one call")
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _stream(stream)
+
+
+def _device(t: torch.Tensor):
+    """Context that makes the tensor's device current (launches go there)."""
+    return contextlib.nullcontext() if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def nsa_full_workspace_size(op: int, heads: Heads, batch: int, total_tokens: int, max_len: int,
+                            max_nodes: int) -> int:
+    return int(lib().nsa_full_workspace_size(op, ctypes.byref(heads), batch, total_tokens, max_len, max_nodes))
+
+
+def nsa_qk_norm_rope(q, k, w_q, w_k, inv_freq, positions, heads: Heads, rope: RopeParams, q_out, k_out, v=None,
+                     v_out=None, cache_rows=None, stream=None):
+    """RMS norm of every query and key head and the rotary position in one pass.
+    q [N, H_q, d_k], k [N, H_kv, d_k], v [N, H_kv, d_v] bf16, packed or views of a
+    fused projection; w_q, w_k fp32 [d_k]; inv_freq fp32 [d_rot/2]; positions device
+    int32 [N]; q_out [N, H_q, d_k]. k_out / v_out [..., H_kv, d]: row n, or row
+    cache_rows[n] (device int64 [N]; outside the cache: not written)."""
+    N = int(q.shape[0])
+    qp, qs = _rows(q, heads.H_q, heads.d_k, "q")
+    kp, ks = _rows(k, heads.H_kv, heads.d_k, "k")
+    vp, vs = _rows(v, heads.H_kv, heads.d_v, "v") if v is not None else (None, 0)
+    _shape(k, (N, heads.H_kv, heads.d_k), "k")
+    if v is not None:
+        _shape(v, (N, heads.H_kv, heads.d_v), "v")
+    _shape(w_q, (heads.d_k,), "w_q")
+    _shape(w_k, (heads.d_k,), "w_k")
+    _shape(positions, (N,), "positions")
+    _shape(cache_rows, (N,), "cache_rows")
+    if rope.d_rot > 0:
+        _shape(inv_freq, (rope.d_rot // 2,), "inv_freq")
+    _shape(q_out, (N, heads.H_q, heads.d_k), "q_out")
+    if tuple(k_out.shape[-2:]) != (heads.H_kv, heads.d_k):
+        raise ValueError(f"k_out: expected [..., {heads.H_kv}, {heads.d_k}], got {tuple(k_out.shape)}")
+    n_rows = k_out.numel() // (heads.H_kv * heads.d_k)
+    if v_out is not None and (tuple(v_out.shape[-2:]) != (heads.H_kv, heads.d_v) or
+                              v_out.numel() != n_rows * heads.H_kv * heads.d_v):
+        raise ValueError("v_out must have the rows of k_out")
+    st = _on(q.device, stream, k, v, w_q, w_k, inv_freq, positions, cache_rows, q_out, k_out, v_out)
+    if N == 0:
+        return
+    with _device(q):
+        s = lib().nsa_qk_norm_rope(qp, qs, kp, ks, vp, vs, _ptr(w_q, torch.float32), _ptr(w_k, torch.float32),
+                                   _ptr(inv_freq, torch.float32) if rope.d_rot > 0 else None,
+                                   _ptr(positions, torch.int32), _ptr(cache_rows, torch.int64), n_rows, N,
+                                   ctypes.byref(heads), ctypes.byref(rope), _ptr(q_out, torch.bfloat16),
+                                   _ptr(k_out, torch.bfloat16), _ptr(v_out, torch.bfloat16), st)
+    _check(s, "nsa_qk_norm_rope")
+
+
+def nsa_qk_norm_rope_backward(q, k, w_q, w_k, inv_freq, positions, dq_out, dk_out, heads: Heads, rope: RopeParams, dq,
+                              dk, dw_q, dw_k, ws, stream=None):
+    """Gradients of nsa_qk_norm_rope: dq_out, dk_out bf16 (of its outputs, packed) in;
+    dq, dk bf16 [N, H, d_k] (packed or views of a fused gradient) and dw_q, dw_k fp32
+    [d_k] out."""
+    N = int(q.shape[0])
+    qp, qs = _rows(q, heads.H_q, heads.d_k, "q")
+    kp, ks = _rows(k, heads.H_kv, heads.d_k, "k")
+    gqp, gqs = _rows(dq, heads.H_q, heads.d_k, "dq")
+    gkp, gks = _rows(dk, heads.H_kv, heads.d_k, "dk")
+    for t, name, h in ((k, "k", heads.H_kv), (dq, "dq", heads.H_q), (dk, "dk", heads.H_kv),
+                       (dq_out, "dq_out", heads.H_q), (dk_out, "dk_out", heads.H_kv)):
+        _shape(t, (N, h, heads.d_k), name)
+    for t, name in ((w_q, "w_q"), (w_k, "w_k"), (dw_q, "dw_q"), (dw_k, "dw_k")):
+        _shape(t, (heads.d_k,), name)
+    _shape(positions, (N,), "positions")
+    if rope.d_rot > 0:
+        _shape(inv_freq, (rope.d_rot // 2,), "inv_freq")
+    f32 = torch.float32
+    st = _on(q.device, stream, k, w_q, w_k, inv_freq, positions, dq_out, dk_out, dq, dk, dw_q, dw_k, ws)
+    if N == 0:   # empty tensors have no address
+        if stream is None:
+            dw_q.zero_()
+            dw_k.zero_()
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(st, device=q.device)):
+                dw_q.zero_()
+                dw_k.zero_()
+        return
+    with _device(q):
+        s = lib().nsa_qk_norm_rope_backward(
+            qp, qs, kp, ks, _ptr(w_q, f32), _ptr(w_k, f32), _ptr(inv_freq, f32) if rope.d_rot > 0 else None,
+            _ptr(positions, torch.int32), N, _ptr(dq_out, torch.bfloat16), _ptr(dk_out, torch.bfloat16),
+            ctypes.byref(heads), ctypes.byref(rope), gqp, gqs, gkp, gks, _ptr(dw_q, f32), _ptr(dw_k, f32), _ptr(ws),
+            ws.numel() * ws.element_size(), st)
+    _check(s, "nsa_qk_norm_rope_backward")
+
+
+def _check_packed(q, k, v, cu_seqlens, heads: Heads):
+    """Shapes of packed prompts against cu_seqlens (host int32 [B + 1])."""
+    B = int(cu_seqlens.numel()) - 1
+    if B < 1:
+        raise ValueError("cu_seqlens needs at least two entries")
+    N = int(cu_seqlens[-1])
+    for t, name, shape in ((q, "q", (heads.H_q, heads.d_k)), (k, "k", (heads.H_kv, heads.d_k)),
+                           (v, "v", (heads.H_kv, heads.d_v))):
+        if t.dim() != 3 or t.shape[0] < N or tuple(t.shape[1:]) != shape:
+            raise ValueError(f"{name}: expected [>= {N}, {shape[0]}, {shape[1]}], got {tuple(t.shape)}")
+    return B, N
+
+
+def nsa_full_prefill(q, k, v, cu_seqlens, heads: Heads, out, lse_out=None, ws=None, scale: float = 0.0, stream=None):
+    """Causal full attention over packed prompts; cu_seqlens host int32 [B+1];
+    out bf16 [N, H_q, d_v]; lse_out fp32 [N, H_q] or None."""
+    B, N = _check_packed(q, k, v, cu_seqlens, heads)
+    if out.dim() != 3 or out.shape[0] < N or tuple(out.shape[1:]) != (heads.H_q, heads.d_v):
+        raise ValueError(f"out: expected [>= {N}, {heads.H_q}, {heads.d_v}], got {tuple(out.shape)}")
+    if lse_out is not None and (lse_out.dim() != 2 or lse_out.shape[0] < N or lse_out.shape[1] != heads.H_q):
+        raise ValueError(f"lse_out: expected [>= {N}, {heads.H_q}], got {tuple(lse_out.shape)}")
+    st = _on(q.device, stream, k, v, out, lse_out, ws)
+    with _device(q):
+        s = lib().nsa_full_prefill(_ptr(q, torch.bfloat16), _ptr(k, torch.bfloat16), _ptr(v, torch.bfloat16),
+                                   _ptr(cu_seqlens, torch.int32, "cpu"), B, ctypes.byref(heads), float(scale),
+                                   _ptr(out, torch.bfloat16), _ptr(lse_out, torch.float32), _ptr(ws),
+                                   ws.numel() * ws.element_size(), st)
+    _check(s, "nsa_full_prefill")
+
+
+def _check_tree(q, cache_lens, n_nodes, tree_mask, heads: Heads, out, lse_out):
+    B, M = int(q.shape[0]), int(q.shape[1])
+    _shape(q, (B, M, heads.H_q, heads.d_k), "q")
+    _shape(cache_lens, (B,), "cache_lens")
+    _shape(n_nodes, (B,), "n_nodes")
+    _shape(tree_mask, (B, M), "tree_mask")
+    _shape(out, (B, M, heads.H_q, heads.d_v), "out")
+    _shape(lse_out, (B, M, heads.H_q), "lse_out")
+    return B, M
+
+
+def nsa_full_tree_decode(q, k_cache, v_cache, cache_lens, n_nodes, tree_mask, max_len: int, heads: Heads, out,
+                         lse_out=None, ws=None, scale: float = 0.0, stream=None):
+    """Full attention of drafted tokens: q [B, M, H_q, d_k], caches [B, Lmax, H_kv, d]
+    that hold the nodes as their last n_nodes[b] tokens; cache_lens, n_nodes (or None)
+    device int32 [B]; tree_mask device int64 [B, M], bit j of word i: node i sees node
+    j (None: a chain)."""
+    B, M = _check_tree(q, cache_lens, n_nodes, tree_mask, heads, out, lse_out)
+    Lmax = int(k_cache.shape[1])
+    _shape(k_cache, (B, Lmax, heads.H_kv, heads.d_k), "k_cache")
+    _shape(v_cache, (B, Lmax, heads.H_kv, heads.d_v), "v_cache")
+    st = _on(q.device, stream, k_cache, v_cache, cache_lens, n_nodes, tree_mask, out, lse_out, ws)
+    with _device(q):
+        s = lib().nsa_full_tree_decode(_ptr(q, torch.bfloat16), _ptr(k_cache, torch.bfloat16),
+                                       _ptr(v_cache, torch.bfloat16), _ptr(cache_lens, torch.int32),
+                                       _ptr(n_nodes, torch.int32), _ptr(tree_mask, torch.int64), B, M, Lmax,
+                                       int(max_len), ctypes.byref(heads), float(scale), _ptr(out, torch.bfloat16),
+                                       _ptr(lse_out, torch.float32), _ptr(ws), ws.numel() * ws.element_size(), st)
+    _check(s, "nsa_full_tree_decode")
+
+
+def nsa_full_tree_decode_paged(q, k_pool, v_pool, block_table, cache_lens, n_nodes, tree_mask, max_len: int,
+                               heads: Heads, out, lse_out=None, ws=None, scale: float = 0.0, stream=None):
+    """nsa_full_tree_decode over pools [n_pages, page_size, H_kv, d] and a device int32
+    block_table [B, max_pages]."""
+    B, M = _check_tree(q, cache_lens, n_nodes, tree_mask, heads, out, lse_out)
+    pages, size = int(k_pool.shape[0]), int(k_pool.shape[1])
+    _shape(k_pool, (pages, size, heads.H_kv, heads.d_k), "k_pool")
+    _shape(v_pool, (pages, size, heads.H_kv, heads.d_v), "v_pool")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table: expected [{B}, max_pages], got {tuple(block_table.shape)}")
+    st = _on(q.device, stream, k_pool, v_pool, block_table, cache_lens, n_nodes, tree_mask, out, lse_out, ws)
+    with _device(q):
+        s = lib().nsa_full_tree_decode_paged(_ptr(q, torch.bfloat16), _ptr(k_pool, torch.bfloat16),
+                                             _ptr(v_pool, torch.bfloat16), pages, size,
+                                             _ptr(block_table, torch.int32), int(block_table.shape[1]),
+                                             _ptr(cache_lens, torch.int32), _ptr(n_nodes, torch.int32),
+                                             _ptr(tree_mask, torch.int64), B, M, int(max_len), ctypes.byref(heads),
+                                             float(scale), _ptr(out, torch.bfloat16), _ptr(lse_out, torch.float32),
+                                             _ptr(ws), ws.numel() * ws.element_size(), st)
+    _check(s, "nsa_full_tree_decode_paged")
 
 
 def nsa_profile_enable(enable: bool):

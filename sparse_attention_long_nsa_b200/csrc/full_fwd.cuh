@@ -1,0 +1,702 @@
+// Full (dense) attention on tcgen05: the kernel behind the causal prompt
+// attention (full_prefill.cu) and the drafted-token attention over a cache
+// (full_tree.cu).
+//
+//   o = softmax(scale q K^T + mask) V,  lse = log sum exp(scale q K^T + mask)
+//
+// A work item ("segment") is a block of query rows of one key head and a run of
+// 128-key tiles. Rows are (token, head of the group): the G heads that share a
+// key head lie in one row block, so a key tile is fetched once for all of them.
+// Scores, the running maximum and the sum stay in fp32; P is rounded to bf16 for
+// the product with V (as the sparse kernels do), the output once at the end.
+//
+// Tensor memory: two score buffers S0, S1 (128 columns each, P written over the
+// columns already read) and two accumulators O0, O1. With NT = 2 the block holds
+// 256 rows, buffer x serves rows 128 x .. + 127, and every key tile is used by
+// both; while one half's softmax runs, the tensor core works for the other. With
+// NT = 1 (128 rows or fewer) both buffers serve the same rows and the key tiles
+// alternate between them; their results are merged at the end.
+//
+// Roles (320 threads): warps 0-3 softmax of buffer 0, warps 4-7 of buffer 1 (a
+// thread owns one row), warp 8 loads Q, K and V by TMA, warp 9 issues the
+// products. K arrives in chunks of 128 keys x 64 channels and V in pieces of the
+// same 16 KB, through one ring in the order of use: the room that is left beside
+// Q holds about one and a half tiles, and a common ring of small pieces keeps
+// more bytes in flight than separate rings of whole tiles would.
+//
+// The product of the tail's V rows past the last key: P is zero there, but 0 x
+// (infinity or NaN) is not, so the issuing warp clears those rows in shared memory
+// first. Every wait is bounded; on a timeout the block stops, lets its copies and
+// products land and leaves.
+#pragma once
+
+#include <limits.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace nsa {
+
+constexpr int kFaThreads = 320;
+constexpr int kFaKeys = 128;
+constexpr int kFaSlot = 16384;
+constexpr float kFaRescaleLog2 = 8.f;   // O is rescaled only when a row max grows by more (log2 units)
+
+template <int DK, int NT>
+struct FaShape {
+  static constexpr int kQBytes = NT * 128 * DK * 2;
+  static constexpr int kMisc = 2048 + (NT == 1 ? 2048 : 0);
+  static constexpr int kFit = (232448 - 1024 - kQBytes - kMisc) / kFaSlot;
+  static constexpr int kSlots = kFit > 12 ? 12 : kFit;
+  static constexpr int kSmem = 1024 + kQBytes + kSlots * kFaSlot + kMisc;
+};
+
+struct FaBars {
+  uint64_t full[12], empty[12];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], drain, merge;
+  uint32_t tmem_base;
+  int abort;
+};
+
+// one work item
+struct FaSeg {
+  int b, g;
+  int i0, ntok;        // first query token (within the sequence) and how many exist from there
+  int kt0, nt[2];      // first key tile; tiles of buffer 0 / 1 (NT = 1: nt[0] = all of them)
+  int nkeys;           // keys in sight of the block: later ones are masked, their V rows cleared
+  int prefix;          // tree: keys below it are seen by every row
+  int64_t q_row;       // row of token i0 in q / out (token units)
+  int64_t kv_row;      // first row of the sequence in k / v (contiguous layouts)
+  int slot;            // >= 0: partial result slot; -1: the item covers all keys, write the output
+};
+
+// ---- schedules: next() gives a block's items in order, the same to every role ----
+
+// Causal prompts: query blocks of NT * 128 / G tokens, longest first over all
+// sequences (each level of tiles names the sequences long enough to have it),
+// dealt to the blocks in snake order.
+template <int NT>
+struct PrefillSched {
+  const FullArgs& a;
+  int it = 0;
+  __device__ explicit PrefillSched(const FullArgs& a_) : a(a_) {}
+  __device__ bool next(FaSeg& s) {
+    const int64_t grid = gridDim.x, c = blockIdx.x;
+    const int64_t x = it * grid + ((it & 1) ? grid - 1 - c : c);
+    ++it;
+    if (x >= a.n_items) return false;
+    const int u = (int)(x / a.H_kv);
+    s.g = (int)(x - (int64_t)u * a.H_kv);
+    int lo = 0, hi = a.seqs.n - 1;   // sequences are sorted by length, longest first
+    while (lo < hi) {                // last i with tile_prefix[i] <= u
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.seqs.tile_prefix[mid] <= u) lo = mid; else hi = mid - 1;
+    }
+    // in the stretch of sequence `lo`, lo + 1 sequences are long enough
+    const int TOK = NT * 128 / a.G, r = u - a.seqs.tile_prefix[lo];
+    const int tile = (a.seqs.len[lo] + TOK - 1) / TOK - 1 - r / (lo + 1);
+    s.b = r % (lo + 1);
+    const int L = a.seqs.len[s.b];
+    s.i0 = tile * TOK;
+    s.ntok = min(TOK, L - s.i0);
+    s.kt0 = 0;
+    s.nkeys = s.i0 + s.ntok;
+    const int n0 = NT == 1 ? s.nkeys : min(s.nkeys, s.i0 + TOK / 2);
+    s.nt[0] = (n0 + kFaKeys - 1) / kFaKeys;
+    s.nt[1] = (NT == 2 && s.ntok > TOK / 2) ? (s.nkeys + kFaKeys - 1) / kFaKeys : 0;
+    s.prefix = 0;
+    s.q_row = a.seqs.tok_off[s.b] + s.i0;
+    s.kv_row = a.seqs.tok_off[s.b];
+    s.slot = -1;
+    return true;
+  }
+};
+
+// Drafted tokens over a cache: all (sequence, key head, row block) units' key
+// tiles in a row, cut into equal runs, one for each block; a unit cut by a
+// border leaves partial results (slot 2 c: the run starts inside the unit; slot
+// 2 c + 1: the unit ends beyond the run) that the merge kernel joins.
+template <int NT>
+struct TreeSched {
+  const FullArgs& a;
+  const int* prefix;   // [B + 1] key tiles of the sequences before
+  int pos, end, b = 0;
+  __device__ TreeSched(const FullArgs& a_, const int* p) : a(a_), prefix(p) {
+    const int64_t W = p[a.B], c = blockIdx.x, n = gridDim.x;
+    pos = (int)(W * c / n);
+    end = (int)(W * (c + 1) / n);
+  }
+  __device__ bool next(FaSeg& s) {
+    if (pos >= end) return false;
+    while (prefix[b + 1] <= pos) ++b;
+    const int L = a.lens[b], n = a.nodes ? a.nodes[b] : a.M;
+    const int TOK = NT * 128 / a.G;
+    const int ntile = (L + kFaKeys - 1) / kFaKeys, rb = (n + TOK - 1) / TOK;
+    const int unit = (pos - prefix[b]) / ntile;
+    s.b = b;
+    s.g = unit / rb;
+    s.i0 = (unit - s.g * rb) * TOK;
+    s.ntok = min(TOK, n - s.i0);
+    s.kt0 = pos - prefix[b] - unit * ntile;
+    const int cnt = min(ntile - s.kt0, end - pos);
+    s.nkeys = L;
+    s.nt[0] = cnt;
+    s.nt[1] = (NT == 2 && s.ntok > TOK / 2) ? cnt : 0;
+    s.prefix = L - n;
+    s.q_row = (int64_t)b * a.M + s.i0;
+    s.kv_row = (int64_t)b * a.Lmax;
+    s.slot = cnt == ntile ? -1 : 2 * (int)blockIdx.x + (s.kt0 == 0 ? 1 : 0);
+    pos += cnt;
+    return true;
+  }
+};
+
+template <int NT, bool TREE>
+struct FaSched : PrefillSched<NT> {
+  __device__ FaSched(const FullArgs& a, const int*) : PrefillSched<NT>(a) {}
+};
+template <int NT>
+struct FaSched<NT, true> : TreeSched<NT> {
+  __device__ FaSched(const FullArgs& a, const int* p) : TreeSched<NT>(a, p) {}
+};
+
+// key tiles of the sequences before each sequence (a sequence with lengths out of
+// range is recorded in the status word and has none)
+template <int NT>
+__device__ __forceinline__ void tree_prefix(const FullArgs& a, int* prefix) {
+  // one warp, four sequences a lane (B <= 128)
+  const int lane = threadIdx.x & 31;
+  int v[4], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = lane * 4 + i;
+    v[i] = 0;
+    if (b < a.B) {
+      const int L = a.lens[b], n = a.nodes ? a.nodes[b] : a.M;
+      if (n < 0 || n > a.M || L < n || L > a.max_len) {
+        if (blockIdx.x == 0 && a.status) {
+          atomicOr(a.status, DEV_ERR_BOUNDS);
+          atomicExch(a.status + 1, 601u);
+        }
+      } else if (n > 0) {
+        const int TOK = NT * 128 / a.G;
+        v[i] = (L + kFaKeys - 1) / kFaKeys * ((n + TOK - 1) / TOK) * a.H_kv;
+      }
+    }
+    sum += v[i];
+  }
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  int run = inc - sum;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = lane * 4 + i;
+    if (b <= a.B) prefix[b] = run;
+    run += v[i];
+    if (b == 127 && a.B == 128) prefix[128] = run;
+  }
+}
+
+template <int DK, int DV, int NT, bool TREE>
+__global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const FullArgs a,
+                                                                      const __grid_constant__ FullMaps mp) {
+  using Sh = FaShape<DK, NT>;
+  constexpr int NS = Sh::kSlots;
+  constexpr int KC = DK / 64;               // ring pieces of a K tile
+  constexpr int VC = DV / 64;               // ring pieces of a V tile: 64 keys x 128 or 128 keys x 64
+  constexpr uint32_t kColO = 256;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* Qs = smem;
+  uint8_t* ring = smem + Sh::kQBytes;
+  FaBars* bars = reinterpret_cast<FaBars*>(ring + NS * kFaSlot);
+  int* prefix = reinterpret_cast<int*>(bars + 1);                                            // [129]
+  float2* ml_s = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(bars) + 2048);         // NT = 1: [2][128]
+  volatile int* abort_flag = &bars->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&bars->full[i], 1);
+      mbar_init(&bars->empty[i], 1);
+    }
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&bars->s_full[x], 1);
+      mbar_init(&bars->p_full[x], 128);
+      mbar_init(&bars->o_full[x], 1);
+    }
+    mbar_init(&bars->drain, 1);
+    mbar_init(&bars->merge, 256);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) tmem_alloc(&bars->tmem_base, 512);
+  if (TREE && warp == 1) tree_prefix<NT>(a, prefix);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  FaSched<NT, TREE> sched(a, prefix);
+  FaSeg sg;
+  bool ok = true;
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0) {
+      prefetch_tmap(&mp.q);
+      prefetch_tmap(&mp.k);
+      prefetch_tmap(&mp.v);
+    }
+    uint32_t pos = 0;      // ring pieces issued
+    int q_n = 0;           // Q tiles issued
+    int blk, brow = 0;     // page table cache: lane i holds the row of 64-key block blk + i
+    while (ok && sched.next(sg)) {
+      blk = INT_MAX;       // another sequence: read anew
+      if (q_n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (q_n - 1) & 1, abort_flag, a.status, 611));
+      if (!ok) break;
+      const int n = max(sg.nt[0], sg.nt[1]);
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bars->q_full, (uint32_t)Sh::kQBytes);
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int kb = 0; kb < KC; ++kb)
+            tma_load_3d(Qs + (x * KC + kb) * 16384, &mp.q, &bars->q_full, kb * 64, sg.g * a.G,
+                        (int)sg.q_row + x * (128 / a.G));
+      }
+      ++q_n;
+      // rows of the two 64-key halves of key tile `t` (the second only if it has keys)
+      auto rows_of = [&](int t, int& r0, int& r1) {
+        const int key = (sg.kt0 + t) * kFaKeys;
+        if (TREE && a.pt.table) {
+          const int kb = key >> 6;
+          if (kb < blk || kb - blk >= 32) {
+            blk = kb;
+            const int e = (kb + lane) * 64;
+            brow = e < sg.nkeys ? (int)paged_row(a.pt, sg.b, e, a.status) : 0;
+          }
+          r0 = __shfl_sync(0xffffffffu, brow, kb - blk);
+          r1 = __shfl_sync(0xffffffffu, brow, (kb - blk + 1) & 31);   // kb - blk is even: never wraps
+        } else {
+          r0 = (int)(sg.kv_row + key);
+          r1 = r0 + 64;
+        }
+      };
+      auto acquire = [&]() -> uint32_t {
+        const uint32_t st = pos % NS;
+        if (pos >= NS)
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->empty[st], ((pos / NS) - 1) & 1, abort_flag, a.status, 612));
+        ++pos;
+        return st;
+      };
+      auto push_k = [&](int t) {
+        int r0, r1;
+        rows_of(t, r0, r1);
+        const bool two = (sg.kt0 + t) * kFaKeys + 64 < sg.nkeys;
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          const uint32_t st = acquire();
+          if (!ok) { --pos; return; }
+          if (lane == 0) {
+            uint8_t* dst = ring + st * kFaSlot;
+            mbar_arrive_expect_tx(&bars->full[st], two ? 16384u : 8192u);
+            tma_load_3d(dst, &mp.k, &bars->full[st], c * 64, sg.g, r0);
+            if (two) tma_load_3d(dst + 8192, &mp.k, &bars->full[st], c * 64, sg.g, r1);
+          }
+        }
+      };
+      auto push_v = [&](int t) {
+        int r0, r1;
+        rows_of(t, r0, r1);
+        const bool two = (sg.kt0 + t) * kFaKeys + 64 < sg.nkeys;
+#pragma unroll
+        for (int c = 0; c < VC; ++c) {
+          const uint32_t st = acquire();
+          if (!ok) { --pos; return; }
+          if (lane == 0) {
+            uint8_t* dst = ring + st * kFaSlot;
+            if (VC == 1) {          // 128 keys x 64 channels
+              mbar_arrive_expect_tx(&bars->full[st], two ? 16384u : 8192u);
+              tma_load_3d(dst, &mp.v, &bars->full[st], 0, sg.g, r0);
+              if (two) tma_load_3d(dst + 8192, &mp.v, &bars->full[st], 0, sg.g, r1);
+            } else if (c == 0 || two) {   // 64 keys x 128 channels
+              mbar_arrive_expect_tx(&bars->full[st], 16384u);
+              tma_load_3d(dst, &mp.v, &bars->full[st], 0, sg.g, c == 0 ? r0 : r1);
+              tma_load_3d(dst + 8192, &mp.v, &bars->full[st], 64, sg.g, c == 0 ? r0 : r1);
+            } else {
+              mbar_arrive(&bars->full[st]);
+            }
+          }
+        }
+      };
+      if (NT == 2) {
+        for (int t = 0; t < n && ok; ++t) {
+          push_k(t);
+          if (ok) push_v(t);
+        }
+      } else {   // K of tile t + 1 before V of tile t
+        push_k(0);
+        for (int t = 0; t < n && ok; ++t) {
+          if (t + 1 < n) push_k(t + 1);
+          if (ok) push_v(t);
+        }
+      }
+    }
+    if (!ok && lane == 0) {   // let the copies still in flight land before the block exits
+      if (q_n > 0) mbar_wait_drain(&bars->q_full, (q_n - 1) & 1);
+      for (uint32_t v = pos < NS ? 0 : pos - NS; v < pos; ++v) mbar_wait_drain(&bars->full[v % NS], (v / NS) & 1);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ products
+    const uint32_t idesc_s = umma_idesc_bf16(128, 128, false, false);
+    const uint32_t idesc_o = umma_idesc_bf16(128, DV, false, true);
+    const uint64_t qdesc = umma_desc_sw128(smem_u32(Qs), 16, 1024);
+    const uint64_t kdesc = umma_desc_sw128(smem_u32(ring), 16, 1024);
+    const uint64_t vdesc = umma_desc_sw128(smem_u32(ring), 8192, 1024);
+    uint32_t base = 0;     // ring piece of the segment's first K chunk
+    int segs = 0;
+    uint32_t p_n[2] = {0, 0};
+    while (ok && sched.next(sg)) {
+      const int n = max(sg.nt[0], sg.nt[1]);
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full, segs & 1, abort_flag, a.status, 621));
+      if (!ok) break;
+      ++segs;
+      tc_fence_after();
+      // S of buffer x = Q (rows of half xq) . K at ring piece p; `rel`: its last use
+      auto qk = [&](int x, int xq, uint32_t p, bool rel) {
+        if (!ok) return;
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          const uint32_t st = (p + c) % NS;
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->full[st], ((p + c) / NS) & 1, abort_flag, a.status, 622));
+          if (!ok) return;
+          if (lane == 0) {
+            tc_fence_after();
+            const uint64_t qd = qdesc + (uint64_t)((xq * KC + c) * (16384 >> 4));
+            const uint64_t kd = kdesc + (uint64_t)(st * (kFaSlot >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_ss(tmem + 128 * x, qd + kk * 2, kd + kk * 2, idesc_s, (c | kk) ? 1u : 0u);
+            if (rel) umma_commit(&bars->empty[st]);
+          }
+        }
+        if (lane == 0) umma_commit(&bars->s_full[x]);
+      };
+      // O of buffer x (+)= P . V of tile t at ring piece p
+      auto pv = [&](int x, int t, uint32_t p, bool first, bool rel) {
+        if (!ok) return;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_full[x], p_n[x] & 1, abort_flag, a.status, 623));
+        ++p_n[x];
+        const int left = sg.nkeys - (sg.kt0 + t) * kFaKeys;   // keys of this tile (may exceed 128)
+#pragma unroll
+        for (int c = 0; c < VC; ++c) {
+          const uint32_t st = (p + c) % NS;
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->full[st], ((p + c) / NS) & 1, abort_flag, a.status, 624));
+          if (!ok) return;
+          uint8_t* vs = ring + st * kFaSlot;
+          const int have = left - c * 64;                      // keys in this piece (VC = 1: of 128)
+          constexpr int kPer = VC == 1 ? 128 : 64;
+          const int rows = have <= 0 ? 0 : (have > 64 || VC == 2) ? kPer : 64;   // rows loaded
+          if (have > 0 && have < rows) {   // clear the rows past the last key
+            for (int i = have * 8 + lane; i < rows * 8; i += 32) {
+              *reinterpret_cast<uint4*>(vs + i * 16) = make_uint4(0, 0, 0, 0);
+              if (VC == 2) *reinterpret_cast<uint4*>(vs + 8192 + i * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) {
+            tc_fence_after();
+            const uint64_t vd = vdesc + (uint64_t)(st * (kFaSlot >> 4));
+#pragma unroll
+            for (int kk = 0; kk < kPer / 16; ++kk)
+              if (kk * 16 < rows)
+                umma_ts(tmem + kColO + 128 * x, tmem + 128 * x + (c * 4 + kk) * 8, vd + kk * (2048 >> 4), idesc_o,
+                        (first && c == 0 && kk == 0) ? 0u : 1u);
+            if (rel) umma_commit(&bars->empty[st]);
+          }
+        }
+      };
+      if (NT == 2) {
+        const int n0 = sg.nt[0], n1 = sg.nt[1];
+        auto kp = [&](int t) { return base + (uint32_t)t * (KC + VC); };
+        auto done_q = [&]() { if (ok && lane == 0) umma_commit(&bars->q_empty); };
+        qk(0, 0, kp(0), n1 == 0);
+        if (n == 1 && n1 == 0) done_q();
+        if (n1 > 0) {
+          qk(1, 1, kp(0), true);
+          if (n1 == 1) done_q();
+        }
+        for (int t = 0; t < n && ok; ++t) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int nx = x == 0 ? n0 : n1;
+            if (t >= nx) continue;
+            const bool rel_v = x == 1 || t >= n1;
+            pv(x, t, kp(t) + KC, t == 0, rel_v);
+            if (t + 1 == nx && ok && lane == 0) umma_commit(&bars->o_full[x]);
+            if (t + 1 < nx) {
+              qk(x, x, kp(t + 1), x == 1 || t + 1 >= n1);
+              if (t + 2 == n && (x == 1 || n1 < n)) done_q();
+            }
+          }
+        }
+        base += (uint32_t)n * (KC + VC);
+      } else {
+        uint32_t p = base;
+        qk(0, 0, p, true);
+        p += KC;
+        for (int t = 0; t < n && ok; ++t) {
+          if (t + 1 < n) {
+            qk((t + 1) & 1, 0, p, true);
+            p += KC;
+          }
+          if ((t + 2 == n || n == 1) && ok && lane == 0) umma_commit(&bars->q_empty);   // the last S is on its way
+          pv(t & 1, t, p, t < 2, true);
+          p += VC;
+          if (t + 2 >= n && ok && lane == 0) umma_commit(&bars->o_full[t & 1]);
+        }
+        base = p;
+      }
+    }
+    // every product has finished before tensor memory is released
+    if (lane == 0) {
+      umma_commit(&bars->drain);
+      mbar_wait_drain(&bars->drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax, output
+    const int x = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;            // row of this buffer = tensor-memory lane
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lane_base + 128 * x;
+    const uint32_t o_col = tmem + lane_base + kColO + 128 * x;
+    const int TOK1 = 128 / a.G;
+    const int xr = NT == 2 ? x : 0;                  // which 128 rows of the block
+    const int tt = xr * TOK1 + r / a.G, hh = r % a.G;
+    const int tt_w0 = xr * TOK1 + (warp & 3) * 32 / a.G;   // first token of the warp's rows
+    const float sc = a.scale_log2;
+    const float thr = kFaRescaleLog2 / sc;
+    uint32_t s_n = 0, o_n[2] = {0, 0}, m_n = 0;
+    auto uwait = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, abort_flag, a.status, site));
+    };
+    while (ok && sched.next(sg)) {
+      const int n = sg.nt[NT == 2 ? x : 0];
+      if (NT == 2 && n == 0) continue;
+      const bool valid = tt < sg.ntok;
+      const bool warp_on = tt_w0 < sg.ntok;          // some row of the warp exists
+      const int t_abs = sg.i0 + tt;                  // prefill: position of the row's token
+      uint64_t bits = 0;
+      if (TREE && valid) {
+        const int nn = sg.nkeys - sg.prefix;         // nodes of the sequence
+        bits = a.mask ? a.mask[(int64_t)sg.b * a.M + t_abs] : (t_abs >= 63 ? ~0ull : (2ull << t_abs) - 1ull);
+        if (nn < 64) bits &= (1ull << nn) - 1ull;
+      }
+      float m = -INFINITY, l = 0.f;
+      bool any = false;                              // this buffer got a tile
+      for (int t = NT == 2 ? 0 : x; t < n; t += NT == 2 ? 1 : 2) {
+        if (ok) ok = uwait(&bars->s_full[x], s_n, 631);
+        if (!ok) break;
+        ++s_n;
+        tc_fence_after();
+        if (warp_on) {
+          float s[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, s + 32 * c);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 128; ++c) asm volatile("" : "+f"(s[c]));   // no use before the wait
+          const int key0 = (sg.kt0 + t) * kFaKeys;
+          if (TREE) {
+            if (key0 + kFaKeys > sg.prefix) {
+#pragma unroll
+              for (int c = 0; c < 128; ++c) {
+                const int j = key0 + c - sg.prefix;
+                const bool see = j < 0 || (j < 64 && ((bits >> (j & 63)) & 1ull));
+                s[c] = see ? s[c] : -INFINITY;
+              }
+            }
+          } else {
+            if (key0 + kFaKeys - 1 > sg.i0 + tt_w0) {
+#pragma unroll
+              for (int c = 0; c < 128; ++c) s[c] = key0 + c <= t_abs ? s[c] : -INFINITY;
+            }
+          }
+          float mx[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = fmaxf(s[i], s[i + 4]);
+#pragma unroll
+          for (int c = 8; c < 128; c += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], fmaxf(s[c + i], s[c + 4 + i]));
+          const float tmx = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          float alpha = 1.f;
+          if (tmx > m + thr) {
+            alpha = ex2((m - tmx) * sc);             // 0 on a row's first visible keys
+            m = tmx;
+          }
+          if (any && __any_sync(0xffffffffu, alpha != 1.f)) {
+            // S of this tile is complete, so the product before it is too
+            for (int c = 0; c < DV; c += 32) {
+              float o[32];
+              tmem_ld32(o_col + c, o);
+              tmem_ld_wait();
+              uint32_t w[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i] * alpha);
+              tmem_st32(o_col + c, w);
+            }
+          }
+          l *= alpha;
+          const float mo = m == -INFINITY ? 0.f : -m * sc;   // nothing in sight yet: p = 2^-inf = 0
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float p0 = ex2(fmaf(s[c + i], sc, mo)), p1 = ex2(fmaf(s[c + i + 1], sc, mo));
+              sum[(i >> 1) & 1] += p0;
+              sum[2 + ((i >> 1) & 1)] += p1;
+              w[i >> 1] = pack_bf16x2(p0, p1);
+            }
+            tmem_st16(s_col + (c >> 1), w);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_wait();
+        }
+        any = true;
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[x]);
+      }
+      if (!ok) break;
+      // ---- the segment's result
+      if (NT == 2) {
+        ok = uwait(&bars->o_full[x], o_n[x], 632);
+        ++o_n[x];
+      } else {
+        ok = uwait(&bars->o_full[0], o_n[0], 633);
+        ++o_n[0];
+        if (ok && n > 1) {
+          ok = uwait(&bars->o_full[1], o_n[1], 634);
+          ++o_n[1];
+        }
+        if (ok) {   // publish (m, l), meet, merge columns x * DV / 2 .. of both accumulators
+          ml_s[x * 128 + r] = make_float2(m, l);
+          mbar_arrive(&bars->merge);
+          ok = uwait(&bars->merge, m_n++, 635);
+        }
+      }
+      if (!ok) break;
+      tc_fence_after();
+      constexpr int NC = NT == 2 ? DV : DV / 2;      // columns this thread writes
+      const int c0 = NT == 2 ? 0 : x * NC;
+      float w0 = 1.f, w1 = 0.f, mm = m, ll = l;
+      if (NT == 1) {
+        const float2 A = ml_s[r], Bv = ml_s[128 + r];
+        mm = fmaxf(A.x, Bv.x);
+        const float mz = mm == -INFINITY ? 0.f : mm;
+        w0 = ex2((A.x - mz) * sc);
+        w1 = n > 1 ? ex2((Bv.x - mz) * sc) : 0.f;
+        ll = A.y * w0 + (n > 1 ? Bv.y * w1 : 0.f);
+      }
+      if (warp_on) {
+        const int64_t row = ((sg.q_row + tt) * a.H_q) + sg.g * a.G + hh;
+        const float inv = sg.slot >= 0 ? 1.f : (ll > 0.f || ll != ll ? 1.f / ll : 0.f);
+        float* po = TREE && sg.slot >= 0 ? a.part + ((int64_t)sg.slot * (NT * 128) + xr * 128 + r) * (DV + 4) : nullptr;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + row * DV;
+#pragma unroll 1
+        for (int c = c0; c < c0 + NC; c += 32) {
+          float o[32];
+          tmem_ld32(tmem + lane_base + kColO + (NT == 2 ? 128 * x : 0) + c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(o[i]));
+          if (NT == 1) {
+            if (n > 1) {
+              float o1[32];
+              tmem_ld32(tmem + lane_base + kColO + 128 + c, o1);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(o1[i]));
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = o[i] * w0 + o1[i] * w1;
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] *= w0;
+            }
+          }
+          if (valid) {
+            if (TREE && po) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4*>(po + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            } else {
+              const bool empty = ll == 0.f;   // no key in sight: zeros
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] = empty ? 0.f : o[i + k] * inv;
+                *reinterpret_cast<uint4*>(dst + c + i) =
+                    make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                               pack_bf16x2(v[6], v[7]));
+              }
+            }
+          }
+        }
+        if (valid && (NT == 2 || x == 0)) {
+          if (TREE && po) {
+            po[DV] = mm * sc;
+            po[DV + 1] = ll;
+          } else if (a.lse) {
+            a.lse[row] = ll == 0.f ? -INFINITY : 0.69314718055994531f * (mm * sc + log2f(ll));
+          }
+        }
+      }
+      if (NT == 1) {   // both accumulators are read before the next segment's products overwrite them
+        tc_fence_before();
+        mbar_arrive(&bars->merge);
+        ok = uwait(&bars->merge, m_n++, 636);
+        tc_fence_after();
+      }
+    }
+  }
+
+  if (TREE && blockIdx.x == 0 && tid < 32) {
+    for (int i = lane; i <= a.B; i += 32) a.prefix_out[i] = prefix[i];
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+template <int DK, int DV, int NT, bool TREE>
+static cudaError_t launch_full_t(const FullArgs& a, const FullMaps& m, int grid, cudaStream_t st) {
+  auto kern = nsa_full_attn_kernel<DK, DV, NT, TREE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, FaShape<DK, NT>::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kFaThreads, FaShape<DK, NT>::kSmem, st>>>(a, m);
+  return cudaGetLastError();
+}
+
+template <int NT, bool TREE>
+static cudaError_t launch_full_d(const FullArgs& a, const FullMaps& m, int grid, cudaStream_t st) {
+  if (a.d_k == 192 && a.d_v == 128) return launch_full_t<192, 128, NT, TREE>(a, m, grid, st);
+  if (a.d_k == 128 && a.d_v == 128) return launch_full_t<128, 128, NT, TREE>(a, m, grid, st);
+  if (a.d_k == 64 && a.d_v == 64) return launch_full_t<64, 64, NT, TREE>(a, m, grid, st);
+  if (a.d_k == 64 && a.d_v == 128) return launch_full_t<64, 128, NT, TREE>(a, m, grid, st);
+  if (a.d_k == 128 && a.d_v == 64) return launch_full_t<128, 64, NT, TREE>(a, m, grid, st);
+  if (a.d_k == 192 && a.d_v == 64) return launch_full_t<192, 64, NT, TREE>(a, m, grid, st);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace nsa

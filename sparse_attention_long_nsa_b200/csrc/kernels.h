@@ -13,7 +13,8 @@ constexpr int kMaxBatch = 128;
 // each launch (see nsa_profile_enable / nsa_profile_read in include/nsa.h).
 enum ProfSlot {
   P_COMPRESS_PREP = 0, P_COMPRESS_GEMM, P_PREFILL_ATTN, P_DEC_CMP, P_DEC_FINE, P_BWD_INDEX, P_BWD_QUERY,
-  P_BWD_KEYS, P_BWD_COMPRESS, P_DSA_INDEX, P_DSA_TOPK, P_DSA_ATTN, P_COUNT
+  P_BWD_KEYS, P_BWD_COMPRESS, P_DSA_INDEX, P_DSA_TOPK, P_DSA_ATTN, P_ROPE,
+  P_ROPE_BWD, P_FULL_ATTN, P_FULL_BWD, P_TREE_ATTN, P_COUNT
 };
 void prof_begin(int slot, cudaStream_t st);
 void set_error_detail(const char* msg);   // text returned by nsa_last_error_detail()
@@ -201,6 +202,66 @@ struct DsaArgs {
   uint32_t* status;
 };
 cudaError_t launch_dsa(const DsaArgs& a, int n_slots, int max_keys, int d_k, int d_v, int d_i, cudaStream_t st);
+
+// ----- per-head norm and rotary position -----
+struct RopeArgs {
+  const void *q, *k, *v;  // bf16 rows of q_stride / k_stride / v_stride elements, heads packed within a row
+  int64_t q_stride, k_stride, v_stride;
+  const float *w_q, *w_k; // fp32 [d_k]
+  const float* inv_freq;  // fp32 [d_rot / 2]
+  const int32_t* positions;   // [N]
+  const int64_t* cache_rows;  // [N] destination rows of keys and values, or null (row n)
+  int64_t n_rows;         // rows of k_out / v_out
+  int64_t N;
+  int H_q, H_kv, H_v;     // H_v: value heads to copy (0 or H_kv)
+  int d_v, d_rot, interleaved;
+  float eps;
+  int tok;                // tokens per block
+  void *q_out, *k_out, *v_out;
+};
+constexpr int kRopeBwdBlocks = 296;   // two per SM
+struct RopeBwdArgs {
+  RopeArgs f;             // q, k, weights, positions (nothing of the outputs)
+  const void *dq_out, *dk_out;   // bf16 [N, H, d_k] gradients of the forward's outputs
+  void *dq, *dk;          // bf16 gradients of the projections, rows of dq_stride / dk_stride
+  int64_t dq_stride, dk_stride;
+  float *dw_q, *dw_k;     // fp32 [d_k]
+  float* part;            // fp32 [kRopeBwdBlocks][d_k]
+  int q_blocks;           // blocks that take the query heads
+};
+cudaError_t launch_qk_norm_rope(RopeArgs a, int d_k, cudaStream_t st);
+cudaError_t launch_qk_norm_rope_bwd(RopeBwdArgs b, int d_k, cudaStream_t st);
+
+// ----- full attention -----
+constexpr int kFullBlocks = 148;      // one persistent block per SM
+struct FullArgs {
+  void* out;              // bf16 [rows, H_q, d_v]
+  float* lse;             // fp32 [rows, H_q] or null
+  int H_q, H_kv, G, d_k, d_v;
+  float scale_log2;       // softmax scale * log2(e)
+  uint32_t* status;
+  // prompts: sequences sorted by length (longest first); tile_prefix[i] = query
+  // blocks of the levels that sequences 0 .. i-1 end in (see PrefillSched)
+  SeqTable seqs;
+  int64_t n_items;        // query blocks x H_kv
+  // drafted tokens over a cache
+  const int32_t* lens;    // [B] tokens in the cache, the nodes included
+  const int32_t* nodes;   // [B] or null (M each)
+  const uint64_t* mask;   // [B, M] or null (a chain)
+  int B, M, Lmax, max_len;
+  PageTable pt;
+  float* part;            // partial results [2 * kFullBlocks][rows][d_v + 4]: O, max (log2 units), sum
+  int32_t* prefix_out;    // [B + 1] key tiles of the sequences before, for the merge
+};
+struct FullMaps {
+  CUtensorMap q;          // box of 128/G tokens x G heads x 64 channels
+  CUtensorMap k, v;       // boxes of 64 rows x 1 head x 64 channels
+};
+cudaError_t launch_full_prefill(const FullArgs& a, const FullMaps& m, int nt, cudaStream_t st);
+cudaError_t launch_full_tree(const FullArgs& a, const FullMaps& m, int nt, cudaStream_t st);
+constexpr size_t full_part_bytes(int nt, int d_v) {
+  return (size_t)2 * kFullBlocks * nt * 128 * (d_v + 4) * 4;
+}
 
 size_t decode_partials_floats(const DecodeArgs& a);
 cudaError_t launch_decode(const DecodeArgs& a, const DecodeMaps& m, cudaStream_t st);

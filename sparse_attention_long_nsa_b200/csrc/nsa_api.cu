@@ -1,6 +1,7 @@
 // C-ABI host layer of libnsa.so: argument validation, workspace carving,
 // tensor-map encoding and the launch sequence of each entry point.
 // See include/nsa.h for the contract of every function.
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -234,7 +235,7 @@ Profiler& prof() {
 
 const char* kSlotNames[P_COUNT] = {"compress_prep", "compress_gemm", "prefill_attn", "dec_cmp", "dec_fine",
                                    "bwd_index", "bwd_query", "bwd_keys", "bwd_compress", "dsa_index", "dsa_topk",
-                                   "dsa_attn"};
+                                   "dsa_attn", "rope", "rope_bwd", "full_attn", "full_bwd", "tree_attn"};
 
 }  // namespace
 
@@ -1079,6 +1080,281 @@ nsa_status_t nsa_dsa_prefill(const void* q, const void* k, const void* v, const 
     if (e != cudaSuccess) return cuda_fail(e, "dsa prefill");
   }
   return NSA_OK;
+}
+
+}  // extern "C"
+
+// ---- full-attention layers ----
+namespace {
+
+bool make_full_maps(FullMaps& m, const void* q, int64_t q_rows, const void* k, const void* v, int64_t kv_rows,
+                    const nsa_heads_t* h) {
+  const int G = h->H_q / h->H_kv;
+  return make_map_3d(&m.q, q, h->d_k, h->H_q, q_rows, G, 128 / G) &&
+         make_map_3d(&m.k, k, h->d_k, h->H_kv, kv_rows, 1, 64) &&
+         make_map_3d(&m.v, v, h->d_v, h->H_kv, kv_rows, 1, 64);
+}
+
+void fill_full_args(FullArgs& a, const nsa_heads_t* h, float scale, void* out, float* lse, void* ws) {
+  a.out = out;
+  a.lse = lse;
+  a.H_q = h->H_q; a.H_kv = h->H_kv; a.G = h->H_q / h->H_kv; a.d_k = h->d_k; a.d_v = h->d_v;
+  a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)h->d_k)) * 1.4426950408889634f;
+  a.status = reinterpret_cast<uint32_t*>(ws);
+}
+
+// the sequences sorted by length, longest first, with the blocks of `tok` tokens
+// level by level (the level of a block is its number within the sequence);
+// returns the number of blocks, -1 for cu_seqlens out of order
+int64_t fill_levels(SeqTable& t, const int32_t* cu_seqlens, int batch, int tok) {
+  int order[NSA_MAX_BATCH];
+  for (int b = 0; b < batch; ++b) {
+    if (cu_seqlens[b + 1] < cu_seqlens[b]) return -1;
+    const int L = cu_seqlens[b + 1] - cu_seqlens[b];
+    int i = b;   // insertion by length, stable
+    for (; i > 0 && cu_seqlens[order[i - 1] + 1] - cu_seqlens[order[i - 1]] < L; --i) order[i] = order[i - 1];
+    order[i] = b;
+  }
+  t.n = batch;
+  int64_t blocks = 0;
+  for (int i = 0; i < batch; ++i) {
+    t.tok_off[i] = cu_seqlens[order[i]];
+    t.len[i] = cu_seqlens[order[i] + 1] - cu_seqlens[order[i]];
+  }
+  for (int i = 0; i < batch; ++i) {
+    t.tile_prefix[i] = (int32_t)blocks;
+    const int64_t here = ((int64_t)t.len[i] + tok - 1) / tok;
+    const int64_t next = i + 1 < batch ? ((int64_t)t.len[i + 1] + tok - 1) / tok : 0;
+    blocks += (here - next) * (i + 1);
+  }
+  t.tile_prefix[batch] = (int32_t)blocks;
+  return blocks;
+}
+
+struct TreeWs {
+  size_t prefix, part, total;
+};
+TreeWs tree_ws(const nsa_heads_t* h, int max_nodes) {
+  TreeWs w{};
+  size_t off = 256;
+  w.prefix = off; off = align256(off + (NSA_MAX_BATCH + 1) * 4);
+  w.part = off; off = align256(off + full_part_bytes(max_nodes * (h->H_q / h->H_kv) > 128 ? 2 : 1, h->d_v));
+  w.total = off;
+  return w;
+}
+
+nsa_status_t check_rope(const nsa_heads_t* heads, const nsa_rope_params_t* rope) {
+  nsa_status_t s = check_heads(heads);
+  if (s != NSA_OK) return s;
+  if (!rope || rope->d_rot < 0 || rope->d_rot > heads->d_k || !(rope->eps > 0.f) || !(rope->eps < INFINITY))
+    return NSA_ERR_INVALID_ARG;
+  return rope->d_rot % 16 == 0 ? NSA_OK : NSA_ERR_UNSUPPORTED;
+}
+
+// rows of `width` packed elements at a stride: aligned, not overlapping
+bool rows_ok(const void* p, int64_t stride, int64_t width) {
+  return p && aligned16(p) && stride >= width && stride % 8 == 0;
+}
+
+nsa_status_t tree_common(const void* q, const void* k, const void* v, const int32_t* cache_lens,
+                         const int32_t* n_nodes, const uint64_t* tree_mask, int32_t batch, int32_t max_nodes,
+                         int32_t Lmax, int32_t max_len, const nsa_heads_t* heads, float scale, void* out,
+                         float* lse_out, void* workspace, size_t ws_bytes, void* stream, const PageTable& pt,
+                         int64_t rows) {
+  nsa_status_t s = check_heads(heads);
+  if (s != NSA_OK) return s;
+  if (batch <= 0 || batch > NSA_MAX_BATCH) return batch <= 0 ? NSA_ERR_INVALID_ARG : NSA_ERR_UNSUPPORTED;
+  if (max_nodes <= 0 || max_nodes > NSA_MAX_NODES) return max_nodes <= 0 ? NSA_ERR_INVALID_ARG : NSA_ERR_UNSUPPORTED;
+  if (!q || !k || !v || !cache_lens || !out || !workspace) return NSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(workspace))
+    return NSA_ERR_INVALID_ARG;
+  if (max_len <= 0 || Lmax < max_len || !(scale >= 0.f) || !(scale < INFINITY)) return NSA_ERR_INVALID_ARG;
+  const int G = heads->H_q / heads->H_kv;
+  const int nt = max_nodes * G > 128 ? 2 : 1, tok = nt * 128 / G;
+  // rows and key tiles are counted in 32 bits on the device
+  if (rows > INT32_MAX ||
+      ((int64_t)max_len + 127) / 128 * ((max_nodes + tok - 1) / tok) * heads->H_kv * batch > INT32_MAX)
+    return NSA_ERR_UNSUPPORTED;
+  const TreeWs w = tree_ws(heads, max_nodes);
+  if (ws_bytes < w.total) return NSA_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  FullArgs a{};
+  fill_full_args(a, heads, scale, out, lse_out, workspace);
+  a.lens = cache_lens;
+  a.nodes = n_nodes;
+  a.mask = tree_mask;
+  a.B = batch; a.M = max_nodes; a.Lmax = Lmax; a.max_len = max_len;
+  a.pt = pt;
+  a.prefix_out = (int32_t*)(ws + w.prefix);
+  a.part = (float*)(ws + w.part);
+  FullMaps m;
+  memset(&m, 0, sizeof(m));
+  if (!make_full_maps(m, q, (int64_t)batch * max_nodes, k, v, rows, heads)) {
+    snprintf(g_detail, sizeof(g_detail), "cuTensorMapEncodeTiled failed");
+    return NSA_ERR_CUDA;
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof_begin(P_TREE_ATTN, st);
+  cudaError_t e = launch_full_tree(a, m, nt, st);
+  prof_end(P_TREE_ATTN, st, 2);
+  return e == cudaSuccess ? NSA_OK : cuda_fail(e, "tree decode");
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t nsa_full_workspace_size(int op, const nsa_heads_t* heads, int32_t batch, int64_t total_tokens,
+                               int32_t max_len, int32_t max_nodes) {
+  if (check_heads(heads) != NSA_OK) return 0;
+  if (batch <= 0 || batch > NSA_MAX_BATCH || total_tokens < 0 || max_len < 0) return 0;
+  switch (op) {
+    case NSA_OP_FULL_PREFILL: return 256;
+    case NSA_OP_TREE_DECODE:
+      if (max_len <= 0 || max_nodes <= 0 || max_nodes > NSA_MAX_NODES) return 0;
+      return tree_ws(heads, max_nodes).total;
+    case NSA_OP_ROPE_BACKWARD: return 256 + align256((size_t)kRopeBwdBlocks * heads->d_k * 4);
+  }
+  return 0;
+}
+
+nsa_status_t nsa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, const float* w_q, const float* w_k, const float* inv_freq,
+                              const int32_t* positions, const int64_t* cache_rows, int64_t n_rows, int64_t N,
+                              const nsa_heads_t* heads, const nsa_rope_params_t* rope, void* q_out, void* k_out,
+                              void* v_out, void* stream) {
+  nsa_status_t s = check_rope(heads, rope);
+  if (s != NSA_OK) return s;
+  if (N < 0 || n_rows < 0 || (!cache_rows && n_rows < N)) return NSA_ERR_INVALID_ARG;
+  if ((v == nullptr) != (v_out == nullptr)) return NSA_ERR_INVALID_ARG;
+  if (!rows_ok(q, q_stride, (int64_t)heads->H_q * heads->d_k) ||
+      !rows_ok(k, k_stride, (int64_t)heads->H_kv * heads->d_k) ||
+      (v && !rows_ok(v, v_stride, (int64_t)heads->H_kv * heads->d_v)))
+    return NSA_ERR_INVALID_ARG;
+  if (!w_q || !w_k || !positions || !q_out || !k_out || (rope->d_rot > 0 && !inv_freq)) return NSA_ERR_INVALID_ARG;
+  if (!aligned16(w_q) || !aligned16(w_k) || !aligned16(q_out) || !aligned16(k_out) || (v_out && !aligned16(v_out)))
+    return NSA_ERR_INVALID_ARG;
+  if (N > INT32_MAX) return NSA_ERR_UNSUPPORTED;
+  if (N == 0) return NSA_OK;
+  RopeArgs a{};
+  a.q = q; a.k = k; a.v = v;
+  a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+  a.w_q = w_q; a.w_k = w_k; a.inv_freq = inv_freq; a.positions = positions;
+  a.cache_rows = cache_rows; a.n_rows = n_rows; a.N = N;
+  a.H_q = heads->H_q; a.H_kv = heads->H_kv; a.H_v = v ? heads->H_kv : 0;
+  a.d_v = heads->d_v; a.d_rot = rope->d_rot; a.interleaved = rope->interleaved; a.eps = rope->eps;
+  a.q_out = q_out; a.k_out = k_out; a.v_out = v_out;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof_begin(P_ROPE, st);
+  cudaError_t e = launch_qk_norm_rope(a, heads->d_k, st);
+  prof_end(P_ROPE, st, 1);
+  return e == cudaSuccess ? NSA_OK : cuda_fail(e, "norm and rotary position");
+}
+
+nsa_status_t nsa_qk_norm_rope_backward(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                       const float* w_q, const float* w_k, const float* inv_freq,
+                                       const int32_t* positions, int64_t N, const void* dq_out, const void* dk_out,
+                                       const nsa_heads_t* heads, const nsa_rope_params_t* rope, void* dq,
+                                       int64_t dq_stride, void* dk, int64_t dk_stride, float* dw_q, float* dw_k,
+                                       void* workspace, size_t ws_bytes, void* stream) {
+  nsa_status_t s = check_rope(heads, rope);
+  if (s != NSA_OK) return s;
+  if (N < 0) return NSA_ERR_INVALID_ARG;
+  const int64_t wq = (int64_t)heads->H_q * heads->d_k, wk = (int64_t)heads->H_kv * heads->d_k;
+  if (!rows_ok(q, q_stride, wq) || !rows_ok(k, k_stride, wk) || !rows_ok(dq, dq_stride, wq) ||
+      !rows_ok(dk, dk_stride, wk))
+    return NSA_ERR_INVALID_ARG;
+  if (!w_q || !w_k || !positions || !dq_out || !dk_out || !dw_q || !dw_k || !workspace ||
+      (rope->d_rot > 0 && !inv_freq))
+    return NSA_ERR_INVALID_ARG;
+  if (!aligned16(w_q) || !aligned16(w_k) || !aligned16(dq_out) || !aligned16(dk_out) || !aligned16(workspace))
+    return NSA_ERR_INVALID_ARG;
+  if (N > INT32_MAX) return NSA_ERR_UNSUPPORTED;
+  if (ws_bytes < 256 + align256((size_t)kRopeBwdBlocks * heads->d_k * 4)) return NSA_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (N == 0) {   // the sums over no tokens
+    cudaError_t e = cudaMemsetAsync(dw_q, 0, (size_t)heads->d_k * 4, st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dw_k, 0, (size_t)heads->d_k * 4, st);
+    return e == cudaSuccess ? NSA_OK : cuda_fail(e, "norm backward memset");
+  }
+  RopeBwdArgs b{};
+  RopeArgs& a = b.f;
+  a.q = q; a.k = k;
+  a.q_stride = q_stride; a.k_stride = k_stride;
+  a.w_q = w_q; a.w_k = w_k; a.inv_freq = inv_freq; a.positions = positions;
+  a.N = N;
+  a.H_q = heads->H_q; a.H_kv = heads->H_kv;
+  a.d_v = heads->d_v; a.d_rot = rope->d_rot; a.interleaved = rope->interleaved; a.eps = rope->eps;
+  b.dq_out = dq_out; b.dk_out = dk_out; b.dq = dq; b.dk = dk;
+  b.dq_stride = dq_stride; b.dk_stride = dk_stride;
+  b.dw_q = dw_q; b.dw_k = dw_k;
+  b.part = (float*)(static_cast<uint8_t*>(workspace) + 256);
+  prof_begin(P_ROPE_BWD, st);
+  cudaError_t e = launch_qk_norm_rope_bwd(b, heads->d_k, st);
+  prof_end(P_ROPE_BWD, st, 2);
+  return e == cudaSuccess ? NSA_OK : cuda_fail(e, "norm and rotary position backward");
+}
+
+nsa_status_t nsa_full_prefill(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int32_t batch,
+                              const nsa_heads_t* heads, float scale, void* out, float* lse_out, void* workspace,
+                              size_t ws_bytes, void* stream) {
+  nsa_status_t s = check_heads(heads);
+  if (s != NSA_OK) return s;
+  if (batch <= 0 || batch > NSA_MAX_BATCH) return batch <= 0 ? NSA_ERR_INVALID_ARG : NSA_ERR_UNSUPPORTED;
+  if (!q || !k || !v || !cu_seqlens || !out || !workspace) return NSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(workspace))
+    return NSA_ERR_INVALID_ARG;
+  if (cu_seqlens[0] != 0 || !(scale >= 0.f) || !(scale < INFINITY)) return NSA_ERR_INVALID_ARG;
+  FullArgs a{};
+  fill_full_args(a, heads, scale, out, lse_out, workspace);
+  // 256 rows a block when that gives every SM one, else 128 rows
+  int nt = 2;
+  int64_t blocks = fill_levels(a.seqs, cu_seqlens, batch, nt * 128 / a.G);
+  if (blocks < 0) return NSA_ERR_INVALID_ARG;
+  if (ws_bytes < 256) return NSA_ERR_WORKSPACE;
+  if (blocks * a.H_kv < kFullBlocks) {
+    nt = 1;
+    blocks = fill_levels(a.seqs, cu_seqlens, batch, nt * 128 / a.G);
+  }
+  a.n_items = blocks * a.H_kv;
+  const int64_t N = cu_seqlens[batch];
+  if (N == 0) return NSA_OK;
+  FullMaps m;
+  memset(&m, 0, sizeof(m));
+  if (!make_full_maps(m, q, N, k, v, N, heads)) {
+    snprintf(g_detail, sizeof(g_detail), "cuTensorMapEncodeTiled failed");
+    return NSA_ERR_CUDA;
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof_begin(P_FULL_ATTN, st);
+  cudaError_t e = launch_full_prefill(a, m, nt, st);
+  prof_end(P_FULL_ATTN, st, 1);
+  return e == cudaSuccess ? NSA_OK : cuda_fail(e, "full attention");
+}
+
+nsa_status_t nsa_full_tree_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* cache_lens,
+                                  const int32_t* n_nodes, const uint64_t* tree_mask, int32_t batch,
+                                  int32_t max_nodes, int32_t Lmax, int32_t max_len, const nsa_heads_t* heads,
+                                  float scale, void* out, float* lse_out, void* workspace, size_t ws_bytes,
+                                  void* stream) {
+  const PageTable none{};
+  return tree_common(q, k_cache, v_cache, cache_lens, n_nodes, tree_mask, batch, max_nodes, Lmax, max_len, heads,
+                     scale, out, lse_out, workspace, ws_bytes, stream, none, (int64_t)batch * Lmax);
+}
+
+nsa_status_t nsa_full_tree_decode_paged(const void* q, const void* k_pool, const void* v_pool, int32_t n_pages,
+                                        int32_t page_size, const int32_t* block_table, int32_t max_pages,
+                                        const int32_t* cache_lens, const int32_t* n_nodes, const uint64_t* tree_mask,
+                                        int32_t batch, int32_t max_nodes, int32_t max_len, const nsa_heads_t* heads,
+                                        float scale, void* out, float* lse_out, void* workspace, size_t ws_bytes,
+                                        void* stream) {
+  if (!block_table || n_pages <= 0 || max_pages <= 0 || page_size <= 0 || page_size % 64 != 0)
+    return NSA_ERR_INVALID_ARG;
+  const int64_t cap = (int64_t)max_pages * page_size;
+  if (cap > INT32_MAX) return NSA_ERR_UNSUPPORTED;
+  const PageTable pt{block_table, page_size, max_pages, n_pages};
+  return tree_common(q, k_pool, v_pool, cache_lens, n_nodes, tree_mask, batch, max_nodes, (int32_t)cap, max_len,
+                     heads, scale, out, lse_out, workspace, ws_bytes, stream, pt, (int64_t)n_pages * page_size);
 }
 
 }  // extern "C"
