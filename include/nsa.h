@@ -459,6 +459,19 @@ nsa_status_t nsa_full_prefill(const void* q, const void* k, const void* v, const
                               const nsa_heads_t* heads, float scale, void* out, float* lse_out, void* workspace,
                               size_t ws_bytes, void* stream);
 
+/* Backward of nsa_full_prefill (its inputs, out and lse_out):
+ *   dout      bf16 [N, H_q, d_v]
+ *   dq, dk, dv bf16 out [N, H_q, d_k], [N, H_kv, d_k], [N, H_kv, d_v], the types of
+ *             the tensors they belong to; sums over keys, rows and the heads that
+ *             share a key head are held in fp32 and rounded once
+ * The same inputs give the same bits. N = 0 launches nothing. Workspace:
+ * nsa_full_workspace_size(NSA_OP_FULL_BACKWARD, heads, batch, N, max_len, 0), which
+ * serves nsa_full_prefill too. */
+nsa_status_t nsa_full_prefill_backward(const void* q, const void* k, const void* v, const void* out, const float* lse,
+                                       const void* dout, const int32_t* cu_seqlens, int32_t batch,
+                                       const nsa_heads_t* heads, float scale, void* dq, void* dk, void* dv,
+                                       void* workspace, size_t ws_bytes, void* stream);
+
 /* Full attention of drafted tokens over a cache that already holds them
  * (speculative decoding). Sequence b has cache_lens[b] tokens in the cache, of
  * which the last n_nodes[b] are the nodes of a tree of drafts, node i in cache row

@@ -36,7 +36,8 @@ EXPORTED = ("nsa_workspace_size", "nsa_workspace_init", "nsa_check_device_status
             "nsa_decode_paged", "nsa_prefill_backward", "nsa_dsa_workspace_size", "nsa_dsa_decode",
             "nsa_dsa_prefill", "nsa_prefill", "nsa_decode", "nsa_profile_enable", "nsa_profile_read", "nsa_profile_slot_name",
             "nsa_status_string", "nsa_last_error_detail", "nsa_full_workspace_size", "nsa_qk_norm_rope",
-            "nsa_qk_norm_rope_backward", "nsa_full_prefill", "nsa_full_tree_decode", "nsa_full_tree_decode_paged")
+            "nsa_qk_norm_rope_backward", "nsa_full_prefill", "nsa_full_prefill_backward", "nsa_full_tree_decode",
+            "nsa_full_tree_decode_paged")
 NSA_PROFILE_SLOTS = 17
 NSA_OP_DSA_DECODE, NSA_OP_DSA_PREFILL = 4, 5
 NSA_OP_FULL_PREFILL, NSA_OP_FULL_BACKWARD, NSA_OP_TREE_DECODE, NSA_OP_ROPE_BACKWARD = 6, 7, 8, 9
@@ -183,6 +184,8 @@ def _load(path: str) -> ctypes.CDLL:
                                             ctypes.POINTER(RopeParams), P, I64, P, I64, P, P, P, SZ, P]
     L.nsa_full_prefill.restype = ctypes.c_int
     L.nsa_full_prefill.argtypes = [P, P, P, P, I32, ctypes.POINTER(Heads), F32, P, P, P, SZ, P]
+    L.nsa_full_prefill_backward.restype = ctypes.c_int
+    L.nsa_full_prefill_backward.argtypes = [P, P, P, P, P, P, P, I32, ctypes.POINTER(Heads), F32, P, P, P, P, SZ, P]
     L.nsa_full_tree_decode.restype = ctypes.c_int
     L.nsa_full_tree_decode.argtypes = [P, P, P, P, P, P, I32, I32, I32, I32, ctypes.POINTER(Heads), F32, P, P, P, SZ,
                                        P]
@@ -568,6 +571,27 @@ def nsa_full_prefill(q, k, v, cu_seqlens, heads: Heads, out, lse_out=None, ws=No
                                    _ptr(out, torch.bfloat16), _ptr(lse_out, torch.float32), _ptr(ws),
                                    ws.numel() * ws.element_size(), st)
     _check(s, "nsa_full_prefill")
+
+
+def nsa_full_prefill_backward(q, k, v, out, lse, dout, cu_seqlens, heads: Heads, dq, dk, dv, ws, scale: float = 0.0,
+                              stream=None):
+    """Gradients of nsa_full_prefill from its inputs, out, lse_out and dout bf16
+    [N, H_q, d_v]: dq, dk, dv bf16, the shapes of q, k, v."""
+    B, N = _check_packed(q, k, v, cu_seqlens, heads)
+    for t, name, shape in ((out, "out", (heads.H_q, heads.d_v)), (dout, "dout", (heads.H_q, heads.d_v)),
+                           (lse, "lse", (heads.H_q,)), (dq, "dq", (heads.H_q, heads.d_k)),
+                           (dk, "dk", (heads.H_kv, heads.d_k)), (dv, "dv", (heads.H_kv, heads.d_v))):
+        if t.dim() != 1 + len(shape) or t.shape[0] < N or tuple(t.shape[1:]) != shape:
+            raise ValueError(f"{name}: expected [>= {N}, ...] with {shape}, got {tuple(t.shape)}")
+    st = _on(q.device, stream, k, v, out, lse, dout, dq, dk, dv, ws)
+    bf = torch.bfloat16
+    with _device(q):
+        s = lib().nsa_full_prefill_backward(_ptr(q, bf), _ptr(k, bf), _ptr(v, bf), _ptr(out, bf),
+                                            _ptr(lse, torch.float32), _ptr(dout, bf),
+                                            _ptr(cu_seqlens, torch.int32, "cpu"), B, ctypes.byref(heads),
+                                            float(scale), _ptr(dq, bf), _ptr(dk, bf), _ptr(dv, bf), _ptr(ws),
+                                            ws.numel() * ws.element_size(), st)
+    _check(s, "nsa_full_prefill_backward")
 
 
 def _check_tree(q, cache_lens, n_nodes, tree_mask, heads: Heads, out, lse_out):

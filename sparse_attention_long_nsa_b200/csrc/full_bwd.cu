@@ -1,0 +1,823 @@
+// Backward of the causal full attention over packed prompts, on tcgen05.
+//
+// With P = exp(scale q K^T - lse) recomputed from the forward's lse,
+//   dV = P^T dO,  dP = dO V^T,  dS = P o (dP - delta),  delta = rowsum(dO o O),
+//   dQ = scale dS K,  dK = scale dS^T Q.
+// P and dS are rounded to bf16 for their products (as P in the forward); sums,
+// delta and the exponent stay in fp32, the results are rounded once.
+//
+// Three kernels, none of which adds into memory that another block adds into, so
+// the results do not depend on timing:
+//   bwd_row     (lse in log2 units, delta) of every row
+//   bwd_kv      a block of 128 keys of one key head against all (token, head) rows
+//               that see it, 128 rows at a time: S^T = K Q^T, dP^T = V dO^T (keys in
+//               the tensor-memory lanes), so that P^T and dS^T are written where they
+//               are the A operand of dV += P^T dO and dK += dS^T Q. The heads that
+//               share the key head are rows like any others.
+//   bwd_q       128 rows against the keys they see: S, dP, dQ += dS K
+// S and dP are formed twice, seven products instead of five: one pass that also
+// accumulated dQ would add fp32 atomics in an order that differs between runs.
+//
+// Tensor memory (512 columns) of bwd_kv: S^T 128, over which P^T (64) is written;
+// dP^T 128 from column 64 on, over which dS^T (64) is written; dV 128, dK 192.
+// bwd_q: S 128, dP 128, dQ 192, dS 64.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace nsa {
+
+namespace {
+
+constexpr int kThreads = 384;   // 8 warps of elementwise work, loads, products, row values, one idle
+constexpr int kPiece = 16384;   // 128 rows x 64 channels, 128-byte swizzled
+constexpr int kRows = 128;
+constexpr int kMaxSlots = 10;
+
+__host__ __device__ constexpr int ring_slots(int dk, int dv) {
+  const int n = (232448 - 1024 - (dk + dv) * 256 - 4096) / kPiece;
+  return n > kMaxSlots ? kMaxSlots : n;
+}
+__host__ __device__ constexpr int bwd_smem(int dk, int dv) {
+  return 1024 + (dk + dv) * 256 + ring_slots(dk, dv) * kPiece + 4096;
+}
+
+struct BwdBars {
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t fix_full, fix_empty;               // the block's resident operands
+  uint64_t s_full, s_read, p_full, dp_full, dp_read, ds_full, ds_free, acc_full, drain;
+  uint64_t row_full[2], row_empty[2];
+  uint32_t tmem_base;
+  int abort;
+};
+
+// zeros from row `from` of a piece on (one warp)
+__device__ __forceinline__ void clear_rows(uint8_t* piece, int from, int lane) {
+  for (int i = from * 8 + lane; i < kRows * 8; i += 32) *reinterpret_cast<uint4*>(piece + i * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// ring cursor of one role
+template <int NS>
+struct Ring {
+  BwdBars* bars;
+  volatile int* abort_flag;
+  uint32_t* status;
+  uint32_t pos = 0;
+  __device__ bool wait_full(uint32_t p, uint32_t site) const {
+    return __all_sync(0xffffffffu, mbar_wait(&bars->full[p % NS], (p / NS) & 1, abort_flag, status, site));
+  }
+  __device__ bool wait_empty(uint32_t p, uint32_t site) const {
+    return p < NS || __all_sync(0xffffffffu, mbar_wait(&bars->empty[p % NS], ((p / NS) - 1) & 1, abort_flag, status, site));
+  }
+};
+
+// dO o O summed over a row, beside the row's lse in log2 units: 8 channels a lane
+template <int DV>
+__global__ void __launch_bounds__(256) nsa_full_bwd_row_kernel(const FullBwdArgs a) {
+  constexpr int L = DV / 8;   // lanes of a row
+  const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / L;
+  const int sub = threadIdx.x % L;
+  if (row >= a.n_rows) return;   // whole rows: the lanes of a row leave together
+  const uint4 o = reinterpret_cast<const uint4*>(a.out)[row * L + sub];
+  const uint4 g = reinterpret_cast<const uint4*>(a.dout)[row * L + sub];
+  const uint32_t ov[4] = {o.x, o.y, o.z, o.w}, gv[4] = {g.x, g.y, g.z, g.w};
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fmaf(__uint_as_float(ov[i] << 16), __uint_as_float(gv[i] << 16), s);
+    s = fmaf(__uint_as_float(ov[i] & 0xffff0000u), __uint_as_float(gv[i] & 0xffff0000u), s);
+  }
+  const uint32_t mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << ((threadIdx.x & 31) & ~(L - 1));
+#pragma unroll
+  for (int w = L / 2; w >= 1; w >>= 1) s += __shfl_xor_sync(mask, s, w);
+  if (sub == 0) a.row[row] = make_float2(a.lse[row] * 1.4426950408889634f, s);
+}
+
+// ---- key blocks: the row tiles of all units in a row, cut into equal runs ----
+struct KvSeg {
+  int b, g, kt;       // sequence, key head, key block
+  int L;              // tokens of the sequence
+  int64_t tok0;       // its first row
+  int r0, n;          // first row tile (of 128 / G tokens) and how many
+  int slot;           // partial slot, -1: the whole unit
+};
+struct KvPlace {
+  int b, g, kt;
+  int64_t start, cnt; // first tile and number of tiles of the unit
+};
+// the unit that holds tile `pos`; a unit of sequence b has R - kt G tiles (R row
+// tiles in the sequence, of which the first kt G lie before the key block)
+__device__ __forceinline__ KvPlace kv_place(const FullBwdArgs& a, int64_t pos) {
+  int lo = 0, hi = a.batch - 1;
+  while (lo < hi) {   // last b with kv_prefix[b] <= pos
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.kv_prefix[mid] <= pos) lo = mid; else hi = mid - 1;
+  }
+  KvPlace p;
+  p.b = lo;
+  const int L = a.len[lo], TOK = kRows / a.G;
+  const int64_t R = (L + TOK - 1) / TOK, T = (L + kRows - 1) / kRows;
+  const int64_t per_g = T * R - (int64_t)a.G * (T * (T - 1) / 2);
+  const int64_t in_b = pos - a.kv_prefix[lo];
+  p.g = (int)(in_b / per_g);
+  const int64_t rem = in_b - p.g * per_g;
+  int k0 = 0, k1 = (int)T - 1;
+  while (k0 < k1) {   // last kt with kt R - G kt (kt - 1) / 2 <= rem
+    const int64_t mid = (k0 + k1 + 1) >> 1;
+    if (mid * R - (int64_t)a.G * (mid * (mid - 1) / 2) <= rem) k0 = (int)mid; else k1 = (int)mid - 1;
+  }
+  p.kt = k0;
+  const int64_t first = (int64_t)k0 * R - (int64_t)a.G * ((int64_t)k0 * (k0 - 1) / 2);
+  p.start = a.kv_prefix[lo] + p.g * per_g + first;
+  p.cnt = R - (int64_t)k0 * a.G;
+  return p;
+}
+__device__ __forceinline__ int64_t run_begin(const FullBwdArgs& a, int c, int blocks) {
+  const int64_t W = a.kv_prefix[a.batch];
+  return W / blocks * c + W % blocks * c / blocks;   // no product of W and c: W may be large
+}
+
+struct KvSched {
+  const FullBwdArgs& a;
+  int64_t pos, end;
+  __device__ explicit KvSched(const FullBwdArgs& a_) : a(a_) {
+    pos = run_begin(a, blockIdx.x, gridDim.x);
+    end = run_begin(a, blockIdx.x + 1, gridDim.x);
+  }
+  __device__ bool next(KvSeg& s) {
+    if (pos >= end) return false;
+    const KvPlace p = kv_place(a, pos);
+    const int64_t off = pos - p.start;
+    const int64_t n = min(p.cnt - off, end - pos);
+    s.b = p.b;
+    s.g = p.g;
+    s.kt = p.kt;
+    s.L = a.len[p.b];
+    s.tok0 = a.tok_off[p.b];
+    s.r0 = p.kt * a.G + (int)off;
+    s.n = (int)n;
+    s.slot = n == p.cnt ? -1 : 2 * (int)blockIdx.x + (off == 0 ? 1 : 0);
+    pos += n;
+    return true;
+  }
+};
+
+__device__ __forceinline__ void bwd_init(BwdBars* bars, int ns) {
+  for (int i = 0; i < ns; ++i) {
+    mbar_init(&bars->full[i], 1);
+    mbar_init(&bars->empty[i], 1);
+  }
+  mbar_init(&bars->fix_full, 1);
+  mbar_init(&bars->fix_empty, 1);
+  mbar_init(&bars->s_full, 1);
+  mbar_init(&bars->s_read, 256);
+  mbar_init(&bars->p_full, 256);
+  mbar_init(&bars->dp_full, 1);
+  mbar_init(&bars->dp_read, 256);
+  mbar_init(&bars->ds_full, 256);
+  mbar_init(&bars->ds_free, 1);
+  mbar_init(&bars->acc_full, 1);
+  mbar_init(&bars->drain, 1);
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&bars->row_full[i], 32);
+    mbar_init(&bars->row_empty[i], 256);
+  }
+  bars->abort = 0;
+  fence_mbar_init();
+}
+
+__device__ __forceinline__ uint4 pack_out(const float* v, float f) {
+  return make_uint4(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f), pack_bf16x2(v[4] * f, v[5] * f),
+                    pack_bf16x2(v[6] * f, v[7] * f));
+}
+
+}  // namespace
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const FullBwdArgs a,
+                                                                      const __grid_constant__ FullBwdMaps mp) {
+  constexpr int KC = DK / 64, VC = DV / 64, NS = ring_slots(DK, DV);
+  constexpr uint32_t kColDP = 64, kColDV = 192, kColDK = 320;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* Ks = smem;                       // K pieces, then V pieces
+  uint8_t* Vs = Ks + KC * kPiece;
+  uint8_t* ring = Vs + VC * kPiece;
+  float2* rowv = reinterpret_cast<float2*>(ring + NS * kPiece);   // [2][128] (lse, delta) of the row tile
+  BwdBars* bars = reinterpret_cast<BwdBars*>(rowv + 2 * kRows);
+  volatile int* abort_flag = &bars->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) bwd_init(bars, NS);
+  if (warp == 0) tmem_alloc(&bars->tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  const int TOK = kRows / a.G;
+  KvSched sched(a);
+  KvSeg sg;
+  bool ok = true;
+  auto uwait = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, abort_flag, a.status, site));
+  };
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ loads
+    Ring<NS> rg{bars, abort_flag, a.status};
+    int segs = 0;
+    while (ok && sched.next(sg)) {
+      if (segs > 0) ok = uwait(&bars->fix_empty, segs - 1, 641);
+      if (!ok) break;
+      if (lane == 0) {
+        const int row = (int)(sg.tok0 + (int64_t)sg.kt * kRows);
+        mbar_arrive_expect_tx(&bars->fix_full, (KC + VC) * kPiece);
+        for (int c = 0; c < KC; ++c) tma_load_3d(Ks + c * kPiece, &mp.k, &bars->fix_full, c * 64, sg.g, row);
+        for (int c = 0; c < VC; ++c) tma_load_3d(Vs + c * kPiece, &mp.v, &bars->fix_full, c * 64, sg.g, row);
+      }
+      ++segs;
+      for (int j = 0; j < sg.n && ok; ++j) {
+        const int row = (int)(sg.tok0 + (int64_t)(sg.r0 + j) * TOK);
+        for (int c = 0; c < VC + KC && ok; ++c) {   // dO before Q
+          ok = rg.wait_empty(rg.pos, 642);
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t st = rg.pos % NS;
+            mbar_arrive_expect_tx(&bars->full[st], kPiece);
+            if (c < VC) tma_load_3d(ring + st * kPiece, &mp.dout, &bars->full[st], c * 64, sg.g * a.G, row);
+            else tma_load_3d(ring + st * kPiece, &mp.q, &bars->full[st], (c - VC) * 64, sg.g * a.G, row);
+          }
+          ++rg.pos;
+        }
+      }
+    }
+    if (!ok && lane == 0) {   // copies in flight land before the block exits
+      if (segs > 0) mbar_wait_drain(&bars->fix_full, (segs - 1) & 1);
+      for (uint32_t v = rg.pos < NS ? 0 : rg.pos - NS; v < rg.pos; ++v)
+        mbar_wait_drain(&bars->full[v % NS], (v / NS) & 1);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ products
+    const uint32_t id_s = umma_idesc_bf16(128, 128, false, false);
+    const uint32_t id_g = umma_idesc_bf16(128, 64, false, true);
+    const uint64_t kd = umma_desc_sw128(smem_u32(Ks), 16, 1024), vd = umma_desc_sw128(smem_u32(Vs), 16, 1024);
+    const uint64_t rd = umma_desc_sw128(smem_u32(ring), 16, 1024);      // rows x channels, K-major
+    Ring<NS> rg{bars, abort_flag, a.status};
+    uint32_t tiles = 0;
+    int segs = 0;
+    while (ok && sched.next(sg)) {
+      ok = uwait(&bars->fix_full, segs, 651);
+      if (!ok) break;
+      ++segs;
+      for (int j = 0; j < sg.n && ok; ++j, ++tiles) {
+        const uint32_t pd = rg.pos, pq = rg.pos + VC;   // ring pieces of dO and Q
+        const int left = min(sg.L - (sg.r0 + j) * TOK, TOK) * a.G;   // rows of the tile that exist
+        // S^T = K Q^T over the P and dS that the products before it have read
+        for (int c = 0; c < KC && ok; ++c) {
+          ok = rg.wait_full(pq + c, 652);
+          if (!ok) break;
+          uint8_t* piece = ring + (pq + c) % NS * kPiece;
+          if (left < kRows) {
+            clear_rows(piece, left, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) {
+            tc_fence_after();
+            const uint64_t q = rd + (uint64_t)((pq + c) % NS * (kPiece >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_ss(tmem, kd + (uint64_t)(c * (kPiece >> 4) + kk * 2), q + kk * 2, id_s, (c | kk) ? 1u : 0u);
+          }
+        }
+        if (!ok) break;
+        if (lane == 0) umma_commit(&bars->s_full);
+        // dP^T = V dO^T beside P: the upper columns of S^T have to be read
+        for (int c = 0; c < VC && ok; ++c) {
+          ok = rg.wait_full(pd + c, 653);
+          if (!ok) break;
+          if (left < kRows) {
+            clear_rows(ring + (pd + c) % NS * kPiece, left, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        ok = ok && uwait(&bars->s_read, tiles, 654);
+        if (!ok) break;
+        if (lane == 0) {
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < VC; ++c) {
+            const uint64_t d = rd + (uint64_t)((pd + c) % NS * (kPiece >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_ss(tmem + kColDP, vd + (uint64_t)(c * (kPiece >> 4) + kk * 2), d + kk * 2, id_s, (c | kk) ? 1u : 0u);
+          }
+          umma_commit(&bars->dp_full);
+          if (j + 1 == sg.n) umma_commit(&bars->fix_empty);
+        }
+        // dV += P^T dO
+        ok = uwait(&bars->p_full, tiles, 655);
+        if (!ok) break;
+        if (lane == 0) {
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < VC; ++c) {
+            const uint64_t d = rd + (uint64_t)((pd + c) % NS * (kPiece >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              umma_ts(tmem + kColDV + 64 * c, tmem + kk * 8, d + (uint64_t)(kk * (2048 >> 4)), id_g, (j | kk) ? 1u : 0u);
+            umma_commit(&bars->empty[(pd + c) % NS]);
+          }
+        }
+        // dK += dS^T Q
+        ok = uwait(&bars->ds_full, tiles, 656);
+        if (!ok) break;
+        if (lane == 0) {
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < KC; ++c) {
+            const uint64_t q = rd + (uint64_t)((pq + c) % NS * (kPiece >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              umma_ts(tmem + kColDK + 64 * c, tmem + kColDP + kk * 8, q + (uint64_t)(kk * (2048 >> 4)), id_g,
+                      (j | kk) ? 1u : 0u);
+            umma_commit(&bars->empty[(pq + c) % NS]);
+          }
+          if (j + 1 == sg.n) umma_commit(&bars->acc_full);
+        }
+        rg.pos += VC + KC;
+      }
+    }
+    if (lane == 0) {   // every product has finished before tensor memory is released
+      umma_commit(&bars->drain);
+      mbar_wait_drain(&bars->drain, 0);
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ (lse, delta) of the row tiles
+    uint32_t tiles = 0;
+    while (ok && sched.next(sg)) {
+      for (int j = 0; j < sg.n && ok; ++j, ++tiles) {
+        const uint32_t st = tiles & 1;
+        if (tiles >= 2) ok = uwait(&bars->row_empty[st], (tiles >> 1) - 1, 661);
+        if (!ok) break;
+        const int t0 = (sg.r0 + j) * TOK;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 32 + lane, t = t0 + r / a.G;
+          rowv[st * kRows + r] = t < sg.L ? a.row[(sg.tok0 + t) * a.H_q + sg.g * a.G + r % a.G] : make_float2(0.f, 0.f);
+        }
+        mbar_arrive(&bars->row_full[st]);
+      }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ P, dS; results
+    const int half = warp >> 2;                      // rows 64 half .. + 63 of the tile
+    const int r = (warp & 3) * 32 + lane;            // key = tensor-memory lane
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const float sc = a.scale_log2;
+    uint32_t tiles = 0;
+    int segs = 0;
+    while (ok && sched.next(sg)) {
+      const int key = sg.kt * kRows + r;
+      for (int j = 0; j < sg.n && ok; ++j, ++tiles) {
+        const int t0 = (sg.r0 + j) * TOK;
+        const bool edge = t0 < sg.kt * kRows + kRows - 1 || t0 + TOK > sg.L;
+        // rows lo <= c < hi of this half see the key
+        const int lo = max(key - t0, 0) * a.G - 64 * half, hi = min(sg.L - t0, TOK) * a.G - 64 * half;
+        const float2* rv = rowv + (tiles & 1) * kRows + 64 * half;
+        ok = uwait(&bars->row_full[tiles & 1], tiles >> 1, 671) && uwait(&bars->s_full, tiles, 672);
+        if (!ok) break;
+        tc_fence_after();
+        float p[64];
+        tmem_ld32(tmem + lane_base + 64 * half, p);
+        tmem_ld32(tmem + lane_base + 64 * half + 32, p + 32);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 64; ++c) asm volatile("" : "+f"(p[c]));   // no use before the wait
+        tc_fence_before();
+        mbar_arrive(&bars->s_read);
+#pragma unroll
+        for (int c = 0; c < 64; c += 2) {
+          const float4 v = *reinterpret_cast<const float4*>(rv + c);
+          p[c] = ex2(fmaf(p[c], sc, -v.x));
+          p[c + 1] = ex2(fmaf(p[c + 1], sc, -v.z));
+        }
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) p[c] = (c >= lo && c < hi) ? p[c] : 0.f;
+        }
+        // P^T lies over columns that the other half's warps read
+        ok = uwait(&bars->s_read, tiles, 673);
+        if (!ok) break;
+        tc_fence_after();
+        {
+          uint32_t w[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+          tmem_st32(tmem + lane_base + 32 * half, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bars->p_full);
+        ok = uwait(&bars->dp_full, tiles, 674);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t w[32];
+#pragma unroll
+        for (int c0 = 0; c0 < 64; c0 += 32) {
+          float d[32];
+          tmem_ld32(tmem + lane_base + kColDP + 64 * half + c0, d);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) asm volatile("" : "+f"(d[c]));
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float4 v = *reinterpret_cast<const float4*>(rv + c0 + c);
+            d[c] = p[c0 + c] * (d[c] - v.y);
+            d[c + 1] = p[c0 + c + 1] * (d[c + 1] - v.w);
+          }
+          if (edge) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) d[c] = (c0 + c >= lo && c0 + c < hi) ? d[c] : 0.f;
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) w[(c0 + c) >> 1] = pack_bf16x2(d[c], d[c + 1]);
+        }
+        tc_fence_before();
+        mbar_arrive(&bars->row_empty[tiles & 1]);
+        mbar_arrive(&bars->dp_read);
+        ok = uwait(&bars->dp_read, tiles, 675);   // dS^T lies over columns that the other half's warps read
+        if (!ok) break;
+        tc_fence_after();
+        tmem_st32(tmem + lane_base + kColDP + 32 * half, w);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bars->ds_full);
+      }
+      if (!ok) break;
+      ok = uwait(&bars->acc_full, segs++, 676);
+      if (!ok) break;
+      tc_fence_after();
+      // warps 0-3 write dV, warps 4-7 dK
+      const int D = half == 0 ? DV : DK;
+      const uint32_t col = half == 0 ? kColDV : kColDK;
+      const float f = half == 0 ? 1.f : a.scale;
+      const bool valid = key < sg.L;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(half == 0 ? a.dv : a.dk) +
+                           ((sg.tok0 + key) * a.H_kv + sg.g) * D;
+      float* part = a.part + ((int64_t)sg.slot * kRows + r) * (DK + DV) + (half == 0 ? 0 : DV);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float d[32];
+        tmem_ld32(tmem + lane_base + col + c, d);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(d[i]));
+        if (valid) {
+          if (sg.slot >= 0) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(part + c + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4*>(dst + c + i) = pack_out(d + i, f);
+          }
+        }
+        __syncwarp();   // the tensor-memory loads are warp-wide
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// The units that a border between runs cut: their parts in block order. Block x:
+// the unit that begins in run x and ends beyond it, 8 keys per block of threads.
+template <int DK, int DV>
+__global__ void __launch_bounds__(256) nsa_full_bwd_merge_kernel(const FullBwdArgs a, int blocks) {
+  constexpr int E = (DK + DV) / 64;   // pairs of channels per lane
+  const int c0 = blockIdx.x;
+  const int64_t lo = run_begin(a, c0, blocks), hi = run_begin(a, c0 + 1, blocks);
+  if (lo >= hi) return;
+  const KvPlace p = kv_place(a, hi - 1);
+  const int64_t end = p.start + p.cnt;
+  if (p.start < lo || end <= hi) return;
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int key = p.kt * kRows + r;
+  if (key >= a.len[p.b]) return;
+  float2 s[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) s[e] = make_float2(0.f, 0.f);
+  for (int c = c0; c < blocks; ++c) {
+    const int64_t b0 = run_begin(a, c, blocks), b1 = run_begin(a, c + 1, blocks);
+    if (b0 >= end) break;
+    if (b0 == b1) continue;
+    const float2* src = reinterpret_cast<const float2*>(
+        a.part + ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * kRows + r) * (DK + DV));
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float2 v = src[e * 32 + lane];
+      s[e].x += v.x;
+      s[e].y += v.y;
+    }
+  }
+  const int64_t row = (a.tok_off[p.b] + key) * a.H_kv + p.g;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {   // channels 0 .. DV - 1: dV, then dK
+    const int ch = e * 64 + lane * 2;
+    if (e * 64 < DV)
+      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.dv) + row * DV + ch) = pack_bf16x2(s[e].x, s[e].y);
+    else
+      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.dk) + row * DK + ch - DV) =
+          pack_bf16x2(s[e].x * a.scale, s[e].y * a.scale);
+  }
+}
+
+// ---- query rows ----
+template <int DK, int DV>
+__global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_q_kernel(const FullBwdArgs a,
+                                                                     const __grid_constant__ FullBwdMaps mp) {
+  constexpr int KC = DK / 64, VC = DV / 64, NS = ring_slots(DK, DV);
+  constexpr uint32_t kColDP = 128, kColDQ = 256, kColDS = 448;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* Qs = smem;                       // Q pieces, then dO pieces
+  uint8_t* Gs = Qs + KC * kPiece;
+  uint8_t* ring = Gs + VC * kPiece;
+  BwdBars* bars = reinterpret_cast<BwdBars*>(ring + NS * kPiece);
+  volatile int* abort_flag = &bars->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) bwd_init(bars, NS);
+  if (warp == 0) tmem_alloc(&bars->tmem_base, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  const int TOK = kRows / a.G;
+  bool ok = true;
+  auto uwait = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, abort_flag, a.status, site));
+  };
+  // items: row tiles, longest first, in snake order (levels as in the forward)
+  int it = 0, b, g, i0, L, nkt;
+  int64_t tok0;
+  auto next = [&]() -> bool {
+    const int64_t grid = gridDim.x, c = blockIdx.x;
+    const int64_t x = it * grid + ((it & 1) ? grid - 1 - c : c);
+    ++it;
+    if (x >= a.n_items) return false;
+    const int u = (int)(x / a.H_kv);
+    g = (int)(x - (int64_t)u * a.H_kv);
+    int lo = 0, hi = a.seqs.n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (a.seqs.tile_prefix[mid] <= u) lo = mid; else hi = mid - 1;
+    }
+    const int rem = u - a.seqs.tile_prefix[lo];
+    const int tile = (a.seqs.len[lo] + TOK - 1) / TOK - 1 - rem / (lo + 1);
+    b = rem % (lo + 1);
+    L = a.seqs.len[b];
+    tok0 = a.seqs.tok_off[b];
+    i0 = tile * TOK;
+    nkt = (min(i0 + TOK, L) + kRows - 1) / kRows;
+    return true;
+  };
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ loads
+    Ring<NS> rg{bars, abort_flag, a.status};
+    int segs = 0;
+    while (ok && next()) {
+      if (segs > 0) ok = uwait(&bars->fix_empty, segs - 1, 681);
+      if (!ok) break;
+      if (lane == 0) {
+        const int row = (int)(tok0 + i0);
+        mbar_arrive_expect_tx(&bars->fix_full, (KC + VC) * kPiece);
+        for (int c = 0; c < KC; ++c) tma_load_3d(Qs + c * kPiece, &mp.q, &bars->fix_full, c * 64, g * a.G, row);
+        for (int c = 0; c < VC; ++c) tma_load_3d(Gs + c * kPiece, &mp.dout, &bars->fix_full, c * 64, g * a.G, row);
+      }
+      ++segs;
+      for (int j = 0; j < nkt && ok; ++j) {
+        const int row = (int)(tok0 + (int64_t)j * kRows);
+        for (int c = 0; c < VC + KC && ok; ++c) {   // V before K
+          ok = rg.wait_empty(rg.pos, 682);
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t st = rg.pos % NS;
+            mbar_arrive_expect_tx(&bars->full[st], kPiece);
+            if (c < VC) tma_load_3d(ring + st * kPiece, &mp.v, &bars->full[st], c * 64, g, row);
+            else tma_load_3d(ring + st * kPiece, &mp.k, &bars->full[st], (c - VC) * 64, g, row);
+          }
+          ++rg.pos;
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      if (segs > 0) mbar_wait_drain(&bars->fix_full, (segs - 1) & 1);
+      for (uint32_t v = rg.pos < NS ? 0 : rg.pos - NS; v < rg.pos; ++v)
+        mbar_wait_drain(&bars->full[v % NS], (v / NS) & 1);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ products
+    // S and dP of tile j + 1 are issued before dQ of tile j: the ring holds
+    // K(j), V(j + 1) and K(j + 1) at once (V(j) is released by its dP)
+    const uint32_t id_s = umma_idesc_bf16(128, 128, false, false);
+    const uint32_t id_g = umma_idesc_bf16(128, 64, false, true);
+    const uint64_t qd = umma_desc_sw128(smem_u32(Qs), 16, 1024), gd = umma_desc_sw128(smem_u32(Gs), 16, 1024);
+    const uint64_t rd = umma_desc_sw128(smem_u32(ring), 16, 1024);
+    Ring<NS> rg{bars, abort_flag, a.status};
+    uint32_t tiles = 0, done = 0;   // S / dP issued; dQ issued
+    int segs = 0;
+    while (ok && next()) {
+      ok = uwait(&bars->fix_full, segs, 691);
+      if (!ok) break;
+      ++segs;
+      const uint32_t base = rg.pos;
+      auto scores = [&](int j) {
+        const uint32_t pv = base + (uint32_t)j * (VC + KC), pk = pv + VC;
+        const int left = min(i0 + TOK, L) - j * kRows;   // keys in sight
+        if (tiles > 0) ok = uwait(&bars->s_read, tiles - 1, 692);
+        for (int c = 0; c < KC && ok; ++c) {
+          ok = rg.wait_full(pk + c, 693);
+          if (!ok) break;
+          if (left < kRows) {   // dS is zero there, but 0 x NaN is not
+            clear_rows(ring + (pk + c) % NS * kPiece, left, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) {
+            tc_fence_after();
+            const uint64_t k = rd + (uint64_t)((pk + c) % NS * (kPiece >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_ss(tmem, qd + (uint64_t)(c * (kPiece >> 4) + kk * 2), k + kk * 2, id_s, (c | kk) ? 1u : 0u);
+          }
+        }
+        if (!ok) return;
+        if (lane == 0) umma_commit(&bars->s_full);
+        if (tiles > 0) ok = uwait(&bars->dp_read, tiles - 1, 694);
+        for (int c = 0; c < VC && ok; ++c) {
+          ok = rg.wait_full(pv + c, 695);
+          if (!ok) break;
+          if (lane == 0) {
+            tc_fence_after();
+            const uint64_t v = rd + (uint64_t)((pv + c) % NS * (kPiece >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_ss(tmem + kColDP, gd + (uint64_t)(c * (kPiece >> 4) + kk * 2), v + kk * 2, id_s, (c | kk) ? 1u : 0u);
+            umma_commit(&bars->empty[(pv + c) % NS]);
+          }
+        }
+        if (!ok) return;
+        if (lane == 0) {
+          umma_commit(&bars->dp_full);
+          if (j + 1 == nkt) umma_commit(&bars->fix_empty);
+        }
+        ++tiles;
+      };
+      scores(0);
+      for (int j = 0; j < nkt && ok; ++j) {
+        if (j + 1 < nkt) scores(j + 1);
+        if (!ok) break;
+        ok = uwait(&bars->ds_full, done, 696);
+        if (!ok) break;
+        ++done;
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t pk = base + (uint32_t)j * (VC + KC) + VC;
+#pragma unroll
+          for (int c = 0; c < KC; ++c) {
+            const uint64_t k = rd + (uint64_t)((pk + c) % NS * (kPiece >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              umma_ts(tmem + kColDQ + 64 * c, tmem + kColDS + kk * 8, k + (uint64_t)(kk * (2048 >> 4)), id_g,
+                      (j | kk) ? 1u : 0u);
+            umma_commit(&bars->empty[(pk + c) % NS]);
+          }
+          umma_commit(&bars->ds_free);
+          if (j + 1 == nkt) umma_commit(&bars->acc_full);
+        }
+      }
+      rg.pos = base + (uint32_t)nkt * (VC + KC);
+    }
+    if (lane == 0) {
+      umma_commit(&bars->drain);
+      mbar_wait_drain(&bars->drain, 0);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ dS; dQ
+    const int half = warp >> 2;                      // keys 64 half .. + 63 of the tile
+    const int r = (warp & 3) * 32 + lane;            // row = tensor-memory lane
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const float sc = a.scale_log2;
+    uint32_t tiles = 0;
+    int segs = 0;
+    while (ok && next()) {
+      const int t = i0 + r / a.G, hq = g * a.G + r % a.G;
+      const bool valid = t < L;
+      const int64_t row = (tok0 + t) * a.H_q + hq;
+      const float2 rv = valid ? a.row[row] : make_float2(0.f, 0.f);
+      for (int j = 0; j < nkt && ok; ++j, ++tiles) {
+        const int k0 = j * kRows + 64 * half;
+        const bool edge = j * kRows + kRows - 1 > i0;   // some key of the tile is past the first token
+        const int hi = t - k0;                          // keys c <= hi are seen
+        ok = uwait(&bars->s_full, tiles, 701);
+        if (!ok) break;
+        tc_fence_after();
+        float p[64];
+        tmem_ld32(tmem + lane_base + 64 * half, p);
+        tmem_ld32(tmem + lane_base + 64 * half + 32, p + 32);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 64; ++c) asm volatile("" : "+f"(p[c]));
+        tc_fence_before();
+        mbar_arrive(&bars->s_read);
+#pragma unroll
+        for (int c = 0; c < 64; ++c) p[c] = ex2(fmaf(p[c], sc, -rv.x));
+        ok = uwait(&bars->dp_full, tiles, 702);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t w[32];
+#pragma unroll
+        for (int c0 = 0; c0 < 64; c0 += 32) {
+          float d[32];
+          tmem_ld32(tmem + lane_base + kColDP + 64 * half + c0, d);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 32; ++c) asm volatile("" : "+f"(d[c]));
+#pragma unroll
+          for (int c = 0; c < 32; ++c) d[c] = p[c0 + c] * (d[c] - rv.y);
+          if (edge) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) d[c] = c0 + c <= hi ? d[c] : 0.f;
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) w[(c0 + c) >> 1] = pack_bf16x2(d[c], d[c + 1]);
+        }
+        tc_fence_before();
+        mbar_arrive(&bars->dp_read);
+        if (tiles > 0) {   // the product that reads the tile before has finished
+          ok = uwait(&bars->ds_free, tiles - 1, 703);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        tmem_st32(tmem + lane_base + kColDS + 32 * half, w);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bars->ds_full);
+      }
+      if (!ok) break;
+      ok = uwait(&bars->acc_full, segs++, 704);
+      if (!ok) break;
+      tc_fence_after();
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dq) + row * DK + half * (DK / 2);
+#pragma unroll 1
+      for (int c = 0; c < DK / 2; c += 32) {
+        float d[32];
+        tmem_ld32(tmem + lane_base + kColDQ + half * (DK / 2) + c, d);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(d[i]));
+        if (valid) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4*>(dst + c + i) = pack_out(d + i, a.scale);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+template <int DK, int DV>
+static cudaError_t launch_bwd_t(const FullBwdArgs& a, const FullBwdMaps& m, cudaStream_t st) {
+  constexpr int smem = bwd_smem(DK, DV);
+  auto kv = nsa_full_bwd_kv_kernel<DK, DV>;
+  auto kq = nsa_full_bwd_q_kernel<DK, DV>;
+  cudaError_t e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t threads = a.n_rows * (DV / 8);
+  nsa_full_bwd_row_kernel<DV><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a);
+  kv<<<kFullBlocks, kThreads, smem, st>>>(a, m);
+  nsa_full_bwd_merge_kernel<DK, DV><<<dim3(kFullBlocks, kRows / 8), 256, 0, st>>>(a, kFullBlocks);
+  const int grid = a.n_items < kFullBlocks ? (int)a.n_items : kFullBlocks;
+  kq<<<grid, kThreads, smem, st>>>(a, m);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_full_bwd(const FullBwdArgs& a, const FullBwdMaps& m, int d_k, int d_v, cudaStream_t st) {
+  if (d_k == 192 && d_v == 128) return launch_bwd_t<192, 128>(a, m, st);
+  if (d_k == 128 && d_v == 128) return launch_bwd_t<128, 128>(a, m, st);
+  if (d_k == 64 && d_v == 64) return launch_bwd_t<64, 64>(a, m, st);
+  if (d_k == 64 && d_v == 128) return launch_bwd_t<64, 128>(a, m, st);
+  if (d_k == 128 && d_v == 64) return launch_bwd_t<128, 64>(a, m, st);
+  if (d_k == 192 && d_v == 64) return launch_bwd_t<192, 64>(a, m, st);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace nsa

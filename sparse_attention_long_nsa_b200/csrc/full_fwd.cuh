@@ -652,6 +652,7 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
               }
             }
           }
+          __syncwarp();   // the tensor-memory loads are warp-wide
         }
         if (valid && (NT == 2 || x == 0)) {
           if (TREE && po) {

@@ -263,6 +263,28 @@ constexpr size_t full_part_bytes(int nt, int d_v) {
   return (size_t)2 * kFullBlocks * nt * 128 * (d_v + 4) * 4;
 }
 
+struct FullBwdArgs {
+  const void *out, *dout; // bf16 [N, H_q, d_v]
+  const float* lse;       // fp32 [N, H_q]
+  float2* row;            // [N, H_q] (lse in log2 units, delta)
+  void *dq, *dk, *dv;     // bf16
+  float* part;            // partial dV, dK of the cut units [2 * kFullBlocks][128][d_v + d_k]
+  int H_q, H_kv, G, batch;
+  float scale, scale_log2;
+  uint32_t* status;
+  int64_t n_rows;         // N * H_q
+  int64_t n_items;        // row tiles x H_kv (query side)
+  int64_t kv_prefix[kMaxBatch + 1];   // row tiles of all key blocks of the sequences before
+  int64_t tok_off[kMaxBatch];         // sequences in packed order (key side)
+  int32_t len[kMaxBatch];
+  SeqTable seqs;          // sorted by length, levels of 128 / G tokens (query side)
+};
+struct FullBwdMaps {
+  CUtensorMap q, dout;    // boxes of 128/G tokens x G heads x 64 channels
+  CUtensorMap k, v;       // boxes of 128 rows x 1 head x 64 channels
+};
+cudaError_t launch_full_bwd(const FullBwdArgs& a, const FullBwdMaps& m, int d_k, int d_v, cudaStream_t st);
+
 size_t decode_partials_floats(const DecodeArgs& a);
 cudaError_t launch_decode(const DecodeArgs& a, const DecodeMaps& m, cudaStream_t st);
 

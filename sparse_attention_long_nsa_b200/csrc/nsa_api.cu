@@ -1143,6 +1143,18 @@ TreeWs tree_ws(const nsa_heads_t* h, int max_nodes) {
   return w;
 }
 
+struct FullBwdWs {
+  size_t row, part, total;
+};
+FullBwdWs full_bwd_ws(const nsa_heads_t* h, int64_t N) {
+  FullBwdWs w{};
+  size_t off = 256;
+  w.row = off; off = align256(off + (size_t)N * h->H_q * 8);
+  w.part = off; off = align256(off + (size_t)2 * kFullBlocks * 128 * (h->d_k + h->d_v) * 4);
+  w.total = off;
+  return w;
+}
+
 nsa_status_t check_rope(const nsa_heads_t* heads, const nsa_rope_params_t* rope) {
   nsa_status_t s = check_heads(heads);
   if (s != NSA_OK) return s;
@@ -1210,6 +1222,7 @@ size_t nsa_full_workspace_size(int op, const nsa_heads_t* heads, int32_t batch, 
   if (batch <= 0 || batch > NSA_MAX_BATCH || total_tokens < 0 || max_len < 0) return 0;
   switch (op) {
     case NSA_OP_FULL_PREFILL: return 256;
+    case NSA_OP_FULL_BACKWARD: return full_bwd_ws(heads, total_tokens).total;
     case NSA_OP_TREE_DECODE:
       if (max_len <= 0 || max_nodes <= 0 || max_nodes > NSA_MAX_NODES) return 0;
       return tree_ws(heads, max_nodes).total;
@@ -1330,6 +1343,62 @@ nsa_status_t nsa_full_prefill(const void* q, const void* k, const void* v, const
   cudaError_t e = launch_full_prefill(a, m, nt, st);
   prof_end(P_FULL_ATTN, st, 1);
   return e == cudaSuccess ? NSA_OK : cuda_fail(e, "full attention");
+}
+
+nsa_status_t nsa_full_prefill_backward(const void* q, const void* k, const void* v, const void* out, const float* lse,
+                                       const void* dout, const int32_t* cu_seqlens, int32_t batch,
+                                       const nsa_heads_t* heads, float scale, void* dq, void* dk, void* dv,
+                                       void* workspace, size_t ws_bytes, void* stream) {
+  nsa_status_t s = check_heads(heads);
+  if (s != NSA_OK) return s;
+  if (batch <= 0 || batch > NSA_MAX_BATCH) return batch <= 0 ? NSA_ERR_INVALID_ARG : NSA_ERR_UNSUPPORTED;
+  if (!q || !k || !v || !out || !lse || !dout || !cu_seqlens || !dq || !dk || !dv || !workspace)
+    return NSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(dout) || !aligned16(dq) ||
+      !aligned16(dk) || !aligned16(dv) || !aligned16(workspace))
+    return NSA_ERR_INVALID_ARG;
+  if (cu_seqlens[0] != 0 || !(scale >= 0.f) || !(scale < INFINITY)) return NSA_ERR_INVALID_ARG;
+  FullBwdArgs a{};
+  a.H_q = heads->H_q; a.H_kv = heads->H_kv; a.G = heads->H_q / heads->H_kv; a.batch = batch;
+  const int tok = 128 / a.G;
+  const int64_t blocks = fill_levels(a.seqs, cu_seqlens, batch, tok);
+  if (blocks < 0) return NSA_ERR_INVALID_ARG;
+  const int64_t N = cu_seqlens[batch];
+  const FullBwdWs w = full_bwd_ws(heads, N);
+  if (ws_bytes < w.total) return NSA_ERR_WORKSPACE;
+  if (N == 0) return NSA_OK;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.out = out; a.dout = dout; a.lse = lse; a.dq = dq; a.dk = dk; a.dv = dv;
+  a.row = (float2*)(ws + w.row);
+  a.part = (float*)(ws + w.part);
+  a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)heads->d_k);
+  a.scale_log2 = a.scale * 1.4426950408889634f;
+  a.status = reinterpret_cast<uint32_t*>(ws);
+  a.n_rows = N * heads->H_q;
+  a.n_items = blocks * heads->H_kv;
+  int64_t tiles = 0;
+  for (int b = 0; b < batch; ++b) {
+    a.tok_off[b] = cu_seqlens[b];
+    a.len[b] = cu_seqlens[b + 1] - cu_seqlens[b];
+    a.kv_prefix[b] = tiles;
+    const int64_t R = ((int64_t)a.len[b] + tok - 1) / tok, T = ((int64_t)a.len[b] + 127) / 128;
+    tiles += (T * R - (int64_t)a.G * (T * (T - 1) / 2)) * heads->H_kv;
+  }
+  a.kv_prefix[batch] = tiles;
+  FullBwdMaps m;
+  memset(&m, 0, sizeof(m));
+  if (!make_map_3d(&m.q, q, heads->d_k, heads->H_q, N, a.G, tok) ||
+      !make_map_3d(&m.dout, dout, heads->d_v, heads->H_q, N, a.G, tok) ||
+      !make_map_3d(&m.k, k, heads->d_k, heads->H_kv, N, 1, 128) ||
+      !make_map_3d(&m.v, v, heads->d_v, heads->H_kv, N, 1, 128)) {
+    snprintf(g_detail, sizeof(g_detail), "cuTensorMapEncodeTiled failed");
+    return NSA_ERR_CUDA;
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  prof_begin(P_FULL_BWD, st);
+  cudaError_t e = launch_full_bwd(a, m, heads->d_k, heads->d_v, st);
+  prof_end(P_FULL_BWD, st, 4);
+  return e == cudaSuccess ? NSA_OK : cuda_fail(e, "full attention backward");
 }
 
 nsa_status_t nsa_full_tree_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* cache_lens,

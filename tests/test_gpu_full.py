@@ -239,6 +239,85 @@ def test_prefill_same_bits_again_on_another_stream_and_replayed():
     assert torch.equal(o3, want) and torch.equal(l3, wl)
 
 
+# ---------------------------------------------------------------- backward of the prompts
+
+def run_backward(q, k, v, cu, h, do, scale=0.0, ws=None):
+    N = int(cu[-1])
+    out, lse = run_prefill(q, k, v, cu, h, scale)
+    g = [torch.full_like(t, 9.0) for t in (q, k, v)]
+    ws = ws_for(nsa.NSA_OP_FULL_BACKWARD, h, cu.numel() - 1, N, N) if ws is None else ws
+    nsa.nsa_full_prefill_backward(q, k, v, out, lse, do, cu, h, *g, ws, scale=scale)
+    nsa.nsa_check_device_status(ws)
+    return g
+
+
+def check_backward(q, k, v, lens, h, do, got, scale):
+    N = sum(lens)
+    want = R.prefill(q[:N], k[:N], v[:N], lens, h.H_kv, scale, do[:N])
+    for t, n in zip(got, ("dq", "dk", "dv")):
+        R.assert_within(t[:N], want[n], want[n + "_tol"], n)
+        assert (t[N:] == 9).all()   # rows behind the last sequence
+
+
+@pytest.mark.parametrize("dims", DIMS)
+@pytest.mark.parametrize("Hq,Hk,lens", [
+    (4, 1, [1]), (16, 1, [129]), (2, 2, [300, 1, 0, 128, 127]), (8, 4, [64, 65, 511]), (16, 2, [513, 40]), (32, 4, [1100, 7, 600])])
+def test_backward(dims, Hq, Hk, lens):
+    h = nsa.Heads(Hq, Hk, *dims)
+    q, k, v, cu = prompt(lens, h, 13, extra=3)
+    do = randn((q.shape[0], Hq, dims[1]), gen(14))
+    check_backward(q, k, v, lens, h, do, run_backward(q, k, v, cu, h, do), dims[0] ** -0.5)
+
+
+def test_backward_long_and_scale():
+    h = nsa.Heads(16, 1, 192, 128)
+    q, k, v, cu = prompt([3000], h, 15)
+    do = randn((3000, 16, 128), gen(16), scale=30)
+    check_backward(q, k, v, [3000], h, do, run_backward(q, k, v, cu, h, do, 0.05), 0.05)
+
+
+def test_backward_nan_of_one_sequence_stays_there():
+    h = nsa.Heads(8, 2, 192, 128)
+    lens = [200, 77, 300]
+    q, k, v, cu = prompt(lens, h, 17, extra=130)
+    do = randn((q.shape[0], 8, 128), gen(18))
+    ref = run_backward(q, k, v, cu, h, do)
+    bad = [t.clone() for t in (q, k, v, do)]
+    for t in bad:
+        t[200:277] = float("nan")
+        t[577:] = float("inf")
+    got = run_backward(bad[0], bad[1], bad[2], cu, h, bad[3])
+    keep = torch.cat([torch.arange(0, 200), torch.arange(277, 577)]).cuda()
+    for a, b in zip(got, ref):
+        assert torch.equal(a[keep], b[keep])
+
+
+def test_backward_same_bits_again_and_replayed():
+    h = nsa.Heads(32, 4, 128, 128)
+    lens = [900, 333]
+    q, k, v, cu = prompt(lens, h, 19)
+    do = randn((1233, 32, 128), gen(20))
+    ref = run_backward(q, k, v, cu, h, do)
+    assert all(torch.equal(a, b) for a, b in zip(ref, run_backward(q, k, v, cu, h, do)))
+    ws = ws_for(nsa.NSA_OP_FULL_BACKWARD, h, 2, 1233, 900)
+    out, lse = torch.empty_like(do), torch.empty((1233, 32), device="cuda")
+    g = [torch.empty_like(t) for t in (q, k, v)]
+
+    def step():
+        nsa.nsa_full_prefill(q, k, v, cu, h, out, lse, ws)   # one workspace for both
+        nsa.nsa_full_prefill_backward(q, k, v, out, lse, do, cu, h, *g, ws)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for t in g:
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ref, g))
+
+
 # ---------------------------------------------------------------- drafted tokens over a cache
 
 def caches(lens, Lmax, h, seed, page=0, poison=True):
