@@ -18,8 +18,9 @@
 // alternate between them; their results are merged at the end.
 //
 // Roles (320 threads): warps 0-3 softmax of buffer 0, warps 4-7 of buffer 1 (a
-// thread owns one row), warp 8 loads Q, K and V by TMA, warp 9 issues the
-// products. K arrives in chunks of 128 keys x 64 channels and V in pieces of the
+// thread owns one row and reads its 128 scores of a tile twice, for the maximum and
+// for the exponentials: all of them do not fit its registers), warp 8 loads Q, K
+// and V by TMA, warp 9 issues the products. K arrives in chunks of 128 keys x 64 channels and V in pieces of the
 // same 16 KB, through one ring in the order of use: the room that is left beside
 // Q holds about one and a half tiles, and a common ring of small pieces keeps
 // more bytes in flight than separate rings of whole tiles would.
@@ -53,7 +54,7 @@ struct FaShape {
 
 struct FaBars {
   uint64_t full[12], empty[12];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], drain, merge;
+  uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_full[2], drain, merge;   // p_full: keys 0-63, 64-127 of a tile
   uint32_t tmem_base;
   int abort;
 };
@@ -228,7 +229,8 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
     mbar_init(&bars->q_empty, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->s_full[x], 1);
-      mbar_init(&bars->p_full[x], 128);
+      mbar_init(&bars->p_full[x][0], 128);
+      mbar_init(&bars->p_full[x][1], 128);
       mbar_init(&bars->o_full[x], 1);
     }
     mbar_init(&bars->drain, 1);
@@ -390,10 +392,8 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
       };
       // O of buffer x (+)= P . V of tile t at ring piece p
       auto pv = [&](int x, int t, uint32_t p, bool first, bool rel) {
-        if (!ok) return;
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_full[x], p_n[x] & 1, abort_flag, a.status, 623));
-        ++p_n[x];
         const int left = sg.nkeys - (sg.kt0 + t) * kFaKeys;   // keys of this tile (may exceed 128)
+        const uint32_t par = p_n[x]++ & 1;
 #pragma unroll
         for (int c = 0; c < VC; ++c) {
           const uint32_t st = (p + c) % NS;
@@ -411,16 +411,21 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (lane == 0) {
-            tc_fence_after();
-            const uint64_t vd = vdesc + (uint64_t)(st * (kFaSlot >> 4));
+          const uint64_t vd = vdesc + (uint64_t)(st * (kFaSlot >> 4));
 #pragma unroll
-            for (int kk = 0; kk < kPer / 16; ++kk)
-              if (kk * 16 < rows)
-                umma_ts(tmem + kColO + 128 * x, tmem + 128 * x + (c * 4 + kk) * 8, vd + kk * (2048 >> 4), idesc_o,
-                        (first && c == 0 && kk == 0) ? 0u : 1u);
-            if (rel) umma_commit(&bars->empty[st]);
+          for (int h = 0; h < 2 / VC; ++h) {   // halves of P in this piece
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->p_full[x][c + h], par, abort_flag, a.status, 623));
+            if (!ok) return;
+            if (lane == 0) {
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                if (kk * 16 < rows)
+                  umma_ts(tmem + kColO + 128 * x, tmem + 128 * x + (c * 4 + kk) * 8, vd + kk * (2048 >> 4), idesc_o,
+                          (first && c == 0 && kk == 0) ? 0u : 1u);
+            }
           }
+          if (rel && lane == 0) umma_commit(&bars->empty[st]);
         }
       };
       if (NT == 2) {
@@ -471,7 +476,7 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
       mbar_wait_drain(&bars->drain, 0);
     }
     __syncwarp();
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------------------------------ softmax, output
     const int x = warp >> 2;
     const int r = (warp & 3) * 32 + lane;            // row of this buffer = tensor-memory lane
@@ -508,36 +513,50 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
         ++s_n;
         tc_fence_after();
         if (warp_on) {
-          float s[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, s + 32 * c);
-          tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < 128; ++c) asm volatile("" : "+f"(s[c]));   // no use before the wait
           const int key0 = (sg.kt0 + t) * kFaKeys;
-          if (TREE) {
-            if (key0 + kFaKeys > sg.prefix) {
+          const bool edge = TREE ? key0 + kFaKeys > sg.prefix : key0 + kFaKeys - 1 > sg.i0 + tt_w0;
+          uint32_t see[4];   // edge tiles: bit c of word i: key key0 + 32 i + c is seen
+          if (edge) {
 #pragma unroll
-              for (int c = 0; c < 128; ++c) {
-                const int j = key0 + c - sg.prefix;
-                const bool see = j < 0 || (j < 64 && ((bits >> (j & 63)) & 1ull));
-                s[c] = see ? s[c] : -INFINITY;
+            for (int i = 0; i < 4; ++i) {
+              if (TREE) {
+                const int j = key0 + 32 * i - sg.prefix;   // node of the first key
+                if (j >= 64) see[i] = 0u;
+                else if (j >= 0) see[i] = (uint32_t)(bits >> j);
+                else if (j > -32) see[i] = ((uint32_t)bits << -j) | ((1u << -j) - 1u);
+                else see[i] = ~0u;
+              } else {
+                const int nv = t_abs + 1 - (key0 + 32 * i);
+                see[i] = nv >= 32 ? ~0u : nv <= 0 ? 0u : (1u << nv) - 1u;
               }
             }
-          } else {
-            if (key0 + kFaKeys - 1 > sg.i0 + tt_w0) {
-#pragma unroll
-              for (int c = 0; c < 128; ++c) s[c] = key0 + c <= t_abs ? s[c] : -INFINITY;
-            }
           }
-          float mx[4];
+          auto hide = [&](float* s, uint32_t word) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = fmaxf(s[i], s[i + 4]);
+            for (int c = 0; c < 32; ++c) s[c] = (word >> c) & 1u ? s[c] : -INFINITY;
+          };
+          float s0[32], s1[32];
+          auto pin = [&](float* s) {   // no use before the wait
 #pragma unroll
-          for (int c = 8; c < 128; c += 8)
+            for (int c = 0; c < 32; ++c) asm volatile("" : "+f"(s[c]));
+          };
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], fmaxf(s[c + i], s[c + 4 + i]));
+          for (int i = 0; i < 4; i += 2) {
+            tmem_ld32(s_col + 32 * i, s0);
+            tmem_ld32(s_col + 32 * i + 32, s1);
+            tmem_ld_wait();
+            pin(s0);
+            pin(s1);
+            if (edge) {
+              hide(s0, see[i]);
+              hide(s1, see[i + 1]);
+            }
+#pragma unroll
+            for (int c = 0; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], fmaxf(s0[c], s1[c]));
+          }
           const float tmx = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          tmem_ld32(s_col, s0);   // the first keys again, beside what follows
           float alpha = 1.f;
           if (tmx > m + thr) {
             alpha = ex2((m - tmx) * sc);             // 0 on a row's first visible keys
@@ -557,25 +576,49 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
           }
           l *= alpha;
           const float mo = m == -INFINITY ? 0.f : -m * sc;   // nothing in sight yet: p = 2^-inf = 0
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < 128; c += 32) {
+          const float2 sc2 = make_float2(sc, sc), mo2 = make_float2(mo, mo);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          auto exps = [&](float* s, int i) {   // P of keys 32 i .. + 31
+            if (edge) hide(s, see[i]);
             uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float p0 = ex2(fmaf(s[c + i], sc, mo)), p1 = ex2(fmaf(s[c + i + 1], sc, mo));
-              sum[(i >> 1) & 1] += p0;
-              sum[2 + ((i >> 1) & 1)] += p1;
-              w[i >> 1] = pack_bf16x2(p0, p1);
+            for (int c = 0; c < 32; c += 2) {
+              const float2 e = fma2(make_float2(s[c], s[c + 1]), sc2, mo2);
+              const float2 p = make_float2(ex2(e.x), ex2(e.y));
+              sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], p);
+              w[c >> 1] = pack_bf16x2(p.x, p.y);
             }
-            tmem_st16(s_col + (c >> 1), w);
-          }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st16(s_col + 16 * i, w);
+          };
+          // P of a quarter goes over scores that have been read: its columns lie below
+          // the quarter's own
+          tmem_ld_wait();
+          pin(s0);
+          tmem_ld32(s_col + 32, s1);
+          exps(s0, 0);
+          tmem_ld_wait();
+          pin(s1);
+          tmem_ld32(s_col + 64, s0);
+          exps(s1, 1);
           tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&bars->p_full[x][0]);   // the product may start on the first 64 keys
+          tmem_ld_wait();
+          pin(s0);
+          tmem_ld32(s_col + 96, s1);
+          exps(s0, 2);
+          tmem_ld_wait();
+          pin(s1);
+          exps(s1, 3);
+          const float2 sm = add2(sum[0], sum[1]);
+          l += sm.x + sm.y;
+          tmem_st_wait();
+        } else {
+          mbar_arrive(&bars->p_full[x][0]);
         }
         any = true;
         tc_fence_before();
-        mbar_arrive(&bars->p_full[x]);
+        mbar_arrive(&bars->p_full[x][1]);
       }
       if (!ok) break;
       // ---- the segment's result
