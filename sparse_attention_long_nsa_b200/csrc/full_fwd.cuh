@@ -17,10 +17,12 @@
 // NT = 1 (128 rows or fewer) both buffers serve the same rows and the key tiles
 // alternate between them; their results are merged at the end.
 //
-// Roles (320 threads): warps 0-3 softmax of buffer 0, warps 4-7 of buffer 1 (a
-// thread owns one row and reads its 128 scores of a tile twice, for the maximum and
-// for the exponentials: all of them do not fit its registers), warp 8 loads Q, K
-// and V by TMA, warp 9 issues the products. K arrives in chunks of 128 keys x 64 channels and V in pieces of the
+// Roles (576 threads): warps 0-7 softmax of buffer 0, warps 8-15 of buffer 1, warp
+// 16 loads Q, K and V by TMA, warp 17 issues the products. A softmax warp owns 16
+// rows; its half-warps hold alternating runs of 32 keys of them and trade maxima and
+// sums by shuffles. With a thread to a whole row (8 warps) the kernel waited on its
+// own latencies: two warps a scheduler issued in 24% of the cycles.
+// K arrives in chunks of 128 keys x 64 channels and V in pieces of the
 // same 16 KB, through one ring in the order of use: the room that is left beside
 // Q holds about one and a half tiles, and a common ring of small pieces keeps
 // more bytes in flight than separate rings of whole tiles would.
@@ -38,7 +40,7 @@
 
 namespace nsa {
 
-constexpr int kFaThreads = 320;
+constexpr int kFaThreads = 576;
 constexpr int kFaKeys = 128;
 constexpr int kFaSlot = 16384;
 constexpr float kFaRescaleLog2 = 8.f;   // O is rescaled only when a row max grows by more (log2 units)
@@ -229,12 +231,12 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
     mbar_init(&bars->q_empty, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->s_full[x], 1);
-      mbar_init(&bars->p_full[x][0], 128);
-      mbar_init(&bars->p_full[x][1], 128);
+      mbar_init(&bars->p_full[x][0], 256);
+      mbar_init(&bars->p_full[x][1], 256);
       mbar_init(&bars->o_full[x], 1);
     }
     mbar_init(&bars->drain, 1);
-    mbar_init(&bars->merge, 256);
+    mbar_init(&bars->merge, 512);
     bars->abort = 0;
     fence_mbar_init();
   }
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
   FaSeg sg;
   bool ok = true;
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ------------------------------------------------------------ loads
     if (lane == 0) {
       prefetch_tmap(&mp.q);
@@ -354,18 +356,21 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
       if (q_n > 0) mbar_wait_drain(&bars->q_full, (q_n - 1) & 1);
       for (uint32_t v = pos < NS ? 0 : pos - NS; v < pos; ++v) mbar_wait_drain(&bars->full[v % NS], (v / NS) & 1);
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ------------------------------------------------------------ products
+    // operands are kept uniform over the warp: as per-lane values each product would
+    // first move six of them, longer than the product itself takes
+    const uint32_t tm = uni(tmem), ring_a = uni(smem_u32(ring)), q_a = uni(smem_u32(Qs));
     const uint32_t idesc_s = umma_idesc_bf16(128, 128, false, false);
     const uint32_t idesc_o = umma_idesc_bf16(128, DV, false, true);
-    const uint64_t qdesc = umma_desc_sw128(smem_u32(Qs), 16, 1024);
-    const uint64_t kdesc = umma_desc_sw128(smem_u32(ring), 16, 1024);
-    const uint64_t vdesc = umma_desc_sw128(smem_u32(ring), 8192, 1024);
+    const uint64_t qdesc = umma_desc_sw128(q_a, 16, 1024);
+    const uint64_t kdesc = umma_desc_sw128(ring_a, 16, 1024);
+    const uint64_t vdesc = umma_desc_sw128(ring_a, 8192, 1024);
     uint32_t base = 0;     // ring piece of the segment's first K chunk
     int segs = 0;
     uint32_t p_n[2] = {0, 0};
     while (ok && sched.next(sg)) {
-      const int n = max(sg.nt[0], sg.nt[1]);
+      const int n0 = uni(sg.nt[0]), n1 = uni(sg.nt[1]), n = max(n0, n1), nkeys = uni(sg.nkeys), kt0 = uni(sg.kt0);
       ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full, segs & 1, abort_flag, a.status, 621));
       if (!ok) break;
       ++segs;
@@ -378,21 +383,21 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
           const uint32_t st = (p + c) % NS;
           ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->full[st], ((p + c) / NS) & 1, abort_flag, a.status, 622));
           if (!ok) return;
-          if (lane == 0) {
+          if (elect_one()) {
             tc_fence_after();
             const uint64_t qd = qdesc + (uint64_t)((xq * KC + c) * (16384 >> 4));
             const uint64_t kd = kdesc + (uint64_t)(st * (kFaSlot >> 4));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_ss(tmem + 128 * x, qd + kk * 2, kd + kk * 2, idesc_s, (c | kk) ? 1u : 0u);
+              umma_ss(tm + 128 * x, qd + kk * 2, kd + kk * 2, idesc_s, (c | kk) ? 1u : 0u);
             if (rel) umma_commit(&bars->empty[st]);
           }
         }
-        if (lane == 0) umma_commit(&bars->s_full[x]);
+        if (elect_one()) umma_commit(&bars->s_full[x]);
       };
       // O of buffer x (+)= P . V of tile t at ring piece p
       auto pv = [&](int x, int t, uint32_t p, bool first, bool rel) {
-        const int left = sg.nkeys - (sg.kt0 + t) * kFaKeys;   // keys of this tile (may exceed 128)
+        const int left = nkeys - (kt0 + t) * kFaKeys;   // keys of this tile (may exceed 128)
         const uint32_t par = p_n[x]++ & 1;
 #pragma unroll
         for (int c = 0; c < VC; ++c) {
@@ -416,22 +421,21 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
           for (int h = 0; h < 2 / VC; ++h) {   // halves of P in this piece
             ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->p_full[x][c + h], par, abort_flag, a.status, 623));
             if (!ok) return;
-            if (lane == 0) {
+            if (elect_one()) {
               tc_fence_after();
 #pragma unroll
               for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
                 if (kk * 16 < rows)
-                  umma_ts(tmem + kColO + 128 * x, tmem + 128 * x + (c * 4 + kk) * 8, vd + kk * (2048 >> 4), idesc_o,
+                  umma_ts(tm + kColO + 128 * x, tm + 128 * x + (c * 4 + kk) * 8, vd + kk * (2048 >> 4), idesc_o,
                           (first && c == 0 && kk == 0) ? 0u : 1u);
             }
           }
-          if (rel && lane == 0) umma_commit(&bars->empty[st]);
+          if (rel && elect_one()) umma_commit(&bars->empty[st]);
         }
       };
       if (NT == 2) {
-        const int n0 = sg.nt[0], n1 = sg.nt[1];
         auto kp = [&](int t) { return base + (uint32_t)t * (KC + VC); };
-        auto done_q = [&]() { if (ok && lane == 0) umma_commit(&bars->q_empty); };
+        auto done_q = [&]() { if (ok && elect_one()) umma_commit(&bars->q_empty); };
         qk(0, 0, kp(0), n1 == 0);
         if (n == 1 && n1 == 0) done_q();
         if (n1 > 0) {
@@ -445,7 +449,7 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
             if (t >= nx) continue;
             const bool rel_v = x == 1 || t >= n1;
             pv(x, t, kp(t) + KC, t == 0, rel_v);
-            if (t + 1 == nx && ok && lane == 0) umma_commit(&bars->o_full[x]);
+            if (t + 1 == nx && ok && elect_one()) umma_commit(&bars->o_full[x]);
             if (t + 1 < nx) {
               qk(x, x, kp(t + 1), x == 1 || t + 1 >= n1);
               if (t + 2 == n && (x == 1 || n1 < n)) done_q();
@@ -462,37 +466,38 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
             qk((t + 1) & 1, 0, p, true);
             p += KC;
           }
-          if ((t + 2 == n || n == 1) && ok && lane == 0) umma_commit(&bars->q_empty);   // the last S is on its way
+          if ((t + 2 == n || n == 1) && ok && elect_one()) umma_commit(&bars->q_empty);   // the last S is on its way
           pv(t & 1, t, p, t < 2, true);
           p += VC;
-          if (t + 2 >= n && ok && lane == 0) umma_commit(&bars->o_full[t & 1]);
+          if (t + 2 >= n && ok && elect_one()) umma_commit(&bars->o_full[t & 1]);
         }
         base = p;
       }
     }
     // every product has finished before tensor memory is released
-    if (lane == 0) {
+    if (elect_one()) {
       umma_commit(&bars->drain);
       mbar_wait_drain(&bars->drain, 0);
     }
     __syncwarp();
-  } else if (warp < 8) {
+  } else {
     // ------------------------------------------------------------ softmax, output
-    const int x = warp >> 2;
-    const int r = (warp & 3) * 32 + lane;            // row of this buffer = tensor-memory lane
-    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const int x = warp >> 3;
+    const int kh = lane >> 4;                        // half-warp
+    const int r = (warp & 3) * 32 + ((warp >> 2) & 1) * 16 + (lane & 15);   // row of this buffer = tensor-memory lane
+    const uint32_t lane_base = (uint32_t)(r - (lane & 15)) << 16;
     const uint32_t s_col = tmem + lane_base + 128 * x;
-    const uint32_t o_col = tmem + lane_base + kColO + 128 * x;
     const int TOK1 = 128 / a.G;
     const int xr = NT == 2 ? x : 0;                  // which 128 rows of the block
     const int tt = xr * TOK1 + r / a.G, hh = r % a.G;
-    const int tt_w0 = xr * TOK1 + (warp & 3) * 32 / a.G;   // first token of the warp's rows
+    const int tt_w0 = xr * TOK1 + (r - (lane & 15)) / a.G;   // first token of the warp's rows
     const float sc = a.scale_log2;
     const float thr = kFaRescaleLog2 / sc;
     uint32_t s_n = 0, o_n[2] = {0, 0}, m_n = 0;
     auto uwait = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, abort_flag, a.status, site));
     };
+    auto other = [&](float v) -> float { return __shfl_xor_sync(0xffffffffu, v, 16); };   // the other half-warp's
     while (ok && sched.next(sg)) {
       const int n = sg.nt[NT == 2 ? x : 0];
       if (NT == 2 && n == 0) continue;
@@ -505,7 +510,7 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
         bits = a.mask ? a.mask[(int64_t)sg.b * a.M + t_abs] : (t_abs >= 63 ? ~0ull : (2ull << t_abs) - 1ull);
         if (nn < 64) bits &= (1ull << nn) - 1ull;
       }
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f;                  // l: this half-warp's keys
       bool any = false;                              // this buffer got a tile
       for (int t = NT == 2 ? 0 : x; t < n; t += NT == 2 ? 1 : 2) {
         if (ok) ok = uwait(&bars->s_full[x], s_n, 631);
@@ -513,50 +518,40 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
         ++s_n;
         tc_fence_after();
         if (warp_on) {
+          // keys 32 kh .. + 31 of the first 64, then of the second 64
+          float s[64];
+          tmem_ld32_h<32>(s_col, s);
+          tmem_ld32_h<32>(s_col + 64, s + 32);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 64; ++c) asm volatile("" : "+f"(s[c]));   // no use before the wait
           const int key0 = (sg.kt0 + t) * kFaKeys;
-          const bool edge = TREE ? key0 + kFaKeys > sg.prefix : key0 + kFaKeys - 1 > sg.i0 + tt_w0;
-          uint32_t see[4];   // edge tiles: bit c of word i: key key0 + 32 i + c is seen
-          if (edge) {
+          if (TREE ? key0 + kFaKeys > sg.prefix : key0 + kFaKeys - 1 > sg.i0 + tt_w0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {            // bit c of `see`: key k0 + c is seen
+              const int k0 = key0 + 64 * i + 32 * kh;
+              uint32_t see;
               if (TREE) {
-                const int j = key0 + 32 * i - sg.prefix;   // node of the first key
-                if (j >= 64) see[i] = 0u;
-                else if (j >= 0) see[i] = (uint32_t)(bits >> j);
-                else if (j > -32) see[i] = ((uint32_t)bits << -j) | ((1u << -j) - 1u);
-                else see[i] = ~0u;
+                const int j = k0 - sg.prefix;        // node of the first key
+                if (j >= 64) see = 0u;
+                else if (j >= 0) see = (uint32_t)(bits >> j);
+                else if (j > -32) see = ((uint32_t)bits << -j) | ((1u << -j) - 1u);
+                else see = ~0u;
               } else {
-                const int nv = t_abs + 1 - (key0 + 32 * i);
-                see[i] = nv >= 32 ? ~0u : nv <= 0 ? 0u : (1u << nv) - 1u;
+                const int nv = t_abs + 1 - k0;
+                see = nv >= 32 ? ~0u : nv <= 0 ? 0u : (1u << nv) - 1u;
               }
+#pragma unroll
+              for (int c = 0; c < 32; ++c) s[32 * i + c] = (see >> c) & 1u ? s[32 * i + c] : -INFINITY;
             }
           }
-          auto hide = [&](float* s, uint32_t word) {
+          float mx[4] = {fmaxf(s[0], s[4]), fmaxf(s[1], s[5]), fmaxf(s[2], s[6]), fmaxf(s[3], s[7])};
 #pragma unroll
-            for (int c = 0; c < 32; ++c) s[c] = (word >> c) & 1u ? s[c] : -INFINITY;
-          };
-          float s0[32], s1[32];
-          auto pin = [&](float* s) {   // no use before the wait
+          for (int c = 8; c < 64; c += 8)
 #pragma unroll
-            for (int c = 0; c < 32; ++c) asm volatile("" : "+f"(s[c]));
-          };
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 4; i += 2) {
-            tmem_ld32(s_col + 32 * i, s0);
-            tmem_ld32(s_col + 32 * i + 32, s1);
-            tmem_ld_wait();
-            pin(s0);
-            pin(s1);
-            if (edge) {
-              hide(s0, see[i]);
-              hide(s1, see[i + 1]);
-            }
-#pragma unroll
-            for (int c = 0; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], fmaxf(s0[c], s1[c]));
-          }
-          const float tmx = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          tmem_ld32(s_col, s0);   // the first keys again, beside what follows
+            for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], fmaxf(s[c + i], s[c + 4 + i]));
+          float tmx = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          tmx = fmaxf(tmx, other(tmx));
           float alpha = 1.f;
           if (tmx > m + thr) {
             alpha = ex2((m - tmx) * sc);             // 0 on a row's first visible keys
@@ -564,64 +559,49 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
           }
           if (any && __any_sync(0xffffffffu, alpha != 1.f)) {
             // S of this tile is complete, so the product before it is too
-            for (int c = 0; c < DV; c += 32) {
-              float o[32];
-              tmem_ld32(o_col + c, o);
+#pragma unroll 1
+            for (int c = 0; c < DV / 2; c += 16) {
+              float o[16];
+              const uint32_t col = tmem + lane_base + kColO + 128 * x + c;
+              tmem_ld16_h<DV / 2>(col, o);
               tmem_ld_wait();
-              uint32_t w[32];
+              uint32_t w[16];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i] * alpha);
-              tmem_st32(o_col + c, w);
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * alpha);
+              tmem_st16_h<DV / 2>(col, w);
             }
           }
           l *= alpha;
           const float mo = m == -INFINITY ? 0.f : -m * sc;   // nothing in sight yet: p = 2^-inf = 0
           const float2 sc2 = make_float2(sc, sc), mo2 = make_float2(mo, mo);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          auto exps = [&](float* s, int i) {   // P of keys 32 i .. + 31
-            if (edge) hide(s, see[i]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
             uint32_t w[16];
 #pragma unroll
             for (int c = 0; c < 32; c += 2) {
-              const float2 e = fma2(make_float2(s[c], s[c + 1]), sc2, mo2);
+              const float2 e = fma2(make_float2(s[32 * i + c], s[32 * i + c + 1]), sc2, mo2);
               const float2 p = make_float2(ex2(e.x), ex2(e.y));
               sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], p);
               w[c >> 1] = pack_bf16x2(p.x, p.y);
             }
-            tmem_st16(s_col + 16 * i, w);
-          };
-          // P of a quarter goes over scores that have been read: its columns lie below
-          // the quarter's own
-          tmem_ld_wait();
-          pin(s0);
-          tmem_ld32(s_col + 32, s1);
-          exps(s0, 0);
-          tmem_ld_wait();
-          pin(s1);
-          tmem_ld32(s_col + 64, s0);
-          exps(s1, 1);
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(&bars->p_full[x][0]);   // the product may start on the first 64 keys
-          tmem_ld_wait();
-          pin(s0);
-          tmem_ld32(s_col + 96, s1);
-          exps(s0, 2);
-          tmem_ld_wait();
-          pin(s1);
-          exps(s1, 3);
+            tmem_st16_h<16>(s_col + 32 * i, w);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&bars->p_full[x][i]);        // the product may start on the first 64 keys
+          }
           const float2 sm = add2(sum[0], sum[1]);
           l += sm.x + sm.y;
-          tmem_st_wait();
         } else {
+          tc_fence_before();
           mbar_arrive(&bars->p_full[x][0]);
+          mbar_arrive(&bars->p_full[x][1]);
         }
         any = true;
-        tc_fence_before();
-        mbar_arrive(&bars->p_full[x][1]);
       }
       if (!ok) break;
       // ---- the segment's result
+      l += other(l);
       if (NT == 2) {
         ok = uwait(&bars->o_full[x], o_n[x], 632);
         ++o_n[x];
@@ -633,15 +613,16 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
           ++o_n[1];
         }
         if (ok) {   // publish (m, l), meet, merge columns x * DV / 2 .. of both accumulators
-          ml_s[x * 128 + r] = make_float2(m, l);
+          if (kh == 0) ml_s[x * 128 + r] = make_float2(m, l);
           mbar_arrive(&bars->merge);
           ok = uwait(&bars->merge, m_n++, 635);
         }
       }
       if (!ok) break;
       tc_fence_after();
-      constexpr int NC = NT == 2 ? DV : DV / 2;      // columns this thread writes
-      const int c0 = NT == 2 ? 0 : x * NC;
+      constexpr int NC = NT == 2 ? DV / 2 : DV / 4;  // columns this thread writes
+      const int c0 = (NT == 2 ? 0 : x * (DV / 2)) + kh * NC;
+      const uint32_t o_base = tmem + lane_base + kColO + (NT == 2 ? 128 * x : x * (DV / 2));
       float w0 = 1.f, w1 = 0.f, mm = m, ll = l;
       if (NT == 1) {
         const float2 A = ml_s[r], Bv = ml_s[128 + r];
@@ -653,56 +634,54 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
       }
       if (warp_on) {
         const int64_t row = ((sg.q_row + tt) * a.H_q) + sg.g * a.G + hh;
-        const float inv = sg.slot >= 0 ? 1.f : (ll > 0.f || ll != ll ? 1.f / ll : 0.f);
+        const bool empty = ll == 0.f;                // no key in sight: zeros
+        const float inv = empty ? 0.f : 1.f / ll;
         float* po = TREE && sg.slot >= 0 ? a.part + ((int64_t)sg.slot * (NT * 128) + xr * 128 + r) * (DV + 4) : nullptr;
         __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + row * DV;
 #pragma unroll 1
-        for (int c = c0; c < c0 + NC; c += 32) {
-          float o[32];
-          tmem_ld32(tmem + lane_base + kColO + (NT == 2 ? 128 * x : 0) + c, o);
+        for (int c = 0; c < NC; c += 16) {
+          float o[16];
+          tmem_ld16_h<NC>(o_base + c, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(o[i]));
+          for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(o[i]));
           if (NT == 1) {
             if (n > 1) {
-              float o1[32];
-              tmem_ld32(tmem + lane_base + kColO + 128 + c, o1);
+              float o1[16];
+              tmem_ld16_h<NC>(o_base + 128 + c, o1);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(o1[i]));
+              for (int i = 0; i < 16; ++i) asm volatile("" : "+f"(o1[i]));
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = o[i] * w0 + o1[i] * w1;
+              for (int i = 0; i < 16; ++i) o[i] = o[i] * w0 + o1[i] * w1;
             } else {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= w0;
+              for (int i = 0; i < 16; ++i) o[i] *= w0;
             }
           }
           if (valid) {
             if (TREE && po) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4*>(po + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4*>(po + c0 + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
             } else {
-              const bool empty = ll == 0.f;   // no key in sight: zeros
 #pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                float v[8];
+              for (int i = 0; i < 16; ++i) o[i] = empty ? 0.f : o[i] * inv;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] = empty ? 0.f : o[i + k] * inv;
-                *reinterpret_cast<uint4*>(dst + c + i) =
-                    make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                               pack_bf16x2(v[6], v[7]));
-              }
+              for (int i = 0; i < 16; i += 8)
+                *reinterpret_cast<uint4*>(dst + c0 + c + i) =
+                    make_uint4(pack_bf16x2(o[i], o[i + 1]), pack_bf16x2(o[i + 2], o[i + 3]),
+                               pack_bf16x2(o[i + 4], o[i + 5]), pack_bf16x2(o[i + 6], o[i + 7]));
             }
           }
           __syncwarp();   // the tensor-memory loads are warp-wide
         }
-        if (valid && (NT == 2 || x == 0)) {
+        if (valid && kh == 0 && (NT == 2 || x == 0)) {
           if (TREE && po) {
             po[DV] = mm * sc;
             po[DV + 1] = ll;
           } else if (a.lse) {
-            a.lse[row] = ll == 0.f ? -INFINITY : 0.69314718055994531f * (mm * sc + log2f(ll));
+            a.lse[row] = empty ? -INFINITY : 0.69314718055994531f * (mm * sc + log2f(ll));
           }
         }
       }
