@@ -375,16 +375,20 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
       if (!ok) break;
       ++segs;
       tc_fence_after();
-      // S of buffer x = Q (rows of half xq) . K at ring piece p; `rel`: its last use
-      auto qk = [&](int x, int xq, uint32_t p, bool rel) {
+      // S of buffer x = Q (rows of half xq) . K at ring piece p; `rel`: its last use;
+      // `fresh`: the pieces have not been waited for yet (all in one round, a lane each)
+      auto qk = [&](int x, int xq, uint32_t p, bool fresh, bool rel) {
         if (!ok) return;
-#pragma unroll
-        for (int c = 0; c < KC; ++c) {
-          const uint32_t st = (p + c) % NS;
-          ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->full[st], ((p + c) / NS) & 1, abort_flag, a.status, 622));
+        if (fresh) {
+          const uint32_t pl = p + lane;
+          ok = __all_sync(0xffffffffu, lane >= KC || mbar_wait(&bars->full[pl % NS], (pl / NS) & 1, abort_flag, a.status, 622));
           if (!ok) return;
-          if (elect_one()) {
-            tc_fence_after();
+        }
+        if (elect_one()) {
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < KC; ++c) {
+            const uint32_t st = (p + c) % NS;
             const uint64_t qd = qdesc + (uint64_t)((xq * KC + c) * (16384 >> 4));
             const uint64_t kd = kdesc + (uint64_t)(st * (kFaSlot >> 4));
 #pragma unroll
@@ -392,54 +396,68 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
               umma_ss(tm + 128 * x, qd + kk * 2, kd + kk * 2, idesc_s, (c | kk) ? 1u : 0u);
             if (rel) umma_commit(&bars->empty[st]);
           }
+          umma_commit(&bars->s_full[x]);
         }
-        if (elect_one()) umma_commit(&bars->s_full[x]);
       };
       // O of buffer x (+)= P . V of tile t at ring piece p
-      auto pv = [&](int x, int t, uint32_t p, bool first, bool rel) {
+      auto pv = [&](int x, int t, uint32_t p, bool fresh, bool rel) {
+        if (!ok) return;
         const int left = nkeys - (kt0 + t) * kFaKeys;   // keys of this tile (may exceed 128)
+        const bool first = t < (NT == 2 ? 1 : 2);
         const uint32_t par = p_n[x]++ & 1;
-#pragma unroll
-        for (int c = 0; c < VC; ++c) {
-          const uint32_t st = (p + c) % NS;
-          ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->full[st], ((p + c) / NS) & 1, abort_flag, a.status, 624));
+        {   // the V pieces and the first half of P
+          const uint32_t pl = p + lane;
+          const bool v = lane < VC;
+          ok = __all_sync(0xffffffffu, (v ? !fresh : lane != 31) ||
+                                           mbar_wait(v ? &bars->full[pl % NS] : &bars->p_full[x][0],
+                                                     v ? (pl / NS) & 1 : par, abort_flag, a.status, 624));
           if (!ok) return;
-          uint8_t* vs = ring + st * kFaSlot;
-          const int have = left - c * 64;                      // keys in this piece (VC = 1: of 128)
-          constexpr int kPer = VC == 1 ? 128 : 64;
-          const int rows = have <= 0 ? 0 : (have > 64 || VC == 2) ? kPer : 64;   // rows loaded
-          if (have > 0 && have < rows) {   // clear the rows past the last key
-            for (int i = have * 8 + lane; i < rows * 8; i += 32) {
-              *reinterpret_cast<uint4*>(vs + i * 16) = make_uint4(0, 0, 0, 0);
-              if (VC == 2) *reinterpret_cast<uint4*>(vs + 8192 + i * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          const uint64_t vd = vdesc + (uint64_t)(st * (kFaSlot >> 4));
+        }
+        constexpr int kPer = VC == 1 ? 128 : 64;        // keys of a piece
+        if (left < kFaKeys && fresh) {                  // clear the rows past the last key
 #pragma unroll
-          for (int h = 0; h < 2 / VC; ++h) {   // halves of P in this piece
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->p_full[x][c + h], par, abort_flag, a.status, 623));
-            if (!ok) return;
-            if (elect_one()) {
-              tc_fence_after();
-#pragma unroll
-              for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                if (kk * 16 < rows)
-                  umma_ts(tm + kColO + 128 * x, tm + 128 * x + (c * 4 + kk) * 8, vd + kk * (2048 >> 4), idesc_o,
-                          (first && c == 0 && kk == 0) ? 0u : 1u);
-            }
+          for (int c = 0; c < VC; ++c) {
+            const int have = left - c * 64;
+            const int rows = VC == 1 && have <= 64 ? 64 : kPer;   // rows loaded
+            uint8_t* vs = ring + (p + c) % NS * kFaSlot;
+            if (have > 0 && have < rows)
+              for (int i = have * 8 + lane; i < rows * 8; i += 32) {
+                *reinterpret_cast<uint4*>(vs + i * 16) = make_uint4(0, 0, 0, 0);
+                if (VC == 2) *reinterpret_cast<uint4*>(vs + 8192 + i * 16) = make_uint4(0, 0, 0, 0);
+              }
           }
-          if (rel && elect_one()) umma_commit(&bars->empty[st]);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        // keys 64 h .. + 63: piece h (VC = 2) or rows 64 h of the one piece
+        auto half = [&](int h) {
+          const uint64_t vd = vdesc + (uint64_t)((p + (VC == 2 ? h : 0)) % NS * (kFaSlot >> 4)) +
+                              (VC == 1 ? (uint64_t)(h * (8192 >> 4)) : 0);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ts(tm + kColO + 128 * x, tm + 128 * x + (h * 4 + kk) * 8, vd + kk * (2048 >> 4), idesc_o,
+                    (first && h == 0 && kk == 0) ? 0u : 1u);
+        };
+        if (elect_one()) {
+          tc_fence_after();
+          half(0);
+          if (VC == 2 && rel) umma_commit(&bars->empty[p % NS]);
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_full[x][1], par, abort_flag, a.status, 623));
+        if (!ok) return;
+        if (elect_one()) {
+          tc_fence_after();
+          if (left > 64) half(1);                       // no keys there: V was not loaded
+          if (rel) umma_commit(&bars->empty[(p + VC - 1) % NS]);
         }
       };
       if (NT == 2) {
         auto kp = [&](int t) { return base + (uint32_t)t * (KC + VC); };
         auto done_q = [&]() { if (ok && elect_one()) umma_commit(&bars->q_empty); };
-        qk(0, 0, kp(0), n1 == 0);
+        qk(0, 0, kp(0), true, n1 == 0);
         if (n == 1 && n1 == 0) done_q();
         if (n1 > 0) {
-          qk(1, 1, kp(0), true);
+          qk(1, 1, kp(0), false, true);
           if (n1 == 1) done_q();
         }
         for (int t = 0; t < n && ok; ++t) {
@@ -447,11 +465,10 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
           for (int x = 0; x < 2; ++x) {
             const int nx = x == 0 ? n0 : n1;
             if (t >= nx) continue;
-            const bool rel_v = x == 1 || t >= n1;
-            pv(x, t, kp(t) + KC, t == 0, rel_v);
+            pv(x, t, kp(t) + KC, x == 0 || t >= n0, x == 1 || t >= n1);
             if (t + 1 == nx && ok && elect_one()) umma_commit(&bars->o_full[x]);
             if (t + 1 < nx) {
-              qk(x, x, kp(t + 1), x == 1 || t + 1 >= n1);
+              qk(x, x, kp(t + 1), x == 0 || t + 1 >= n0, x == 1 || t + 1 >= n1);
               if (t + 2 == n && (x == 1 || n1 < n)) done_q();
             }
           }
@@ -459,15 +476,15 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
         base += (uint32_t)n * (KC + VC);
       } else {
         uint32_t p = base;
-        qk(0, 0, p, true);
+        qk(0, 0, p, true, true);
         p += KC;
         for (int t = 0; t < n && ok; ++t) {
           if (t + 1 < n) {
-            qk((t + 1) & 1, 0, p, true);
+            qk((t + 1) & 1, 0, p, true, true);
             p += KC;
           }
           if ((t + 2 == n || n == 1) && ok && elect_one()) umma_commit(&bars->q_empty);   // the last S is on its way
-          pv(t & 1, t, p, t < 2, true);
+          pv(t & 1, t, p, true, true);
           p += VC;
           if (t + 2 >= n && ok && elect_one()) umma_commit(&bars->o_full[t & 1]);
         }
