@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
     const uint64_t vdesc = umma_desc_sw128(ring_a, 8192, 1024);
     uint32_t base = 0;     // ring piece of the segment's first K chunk
     int segs = 0;
-    uint32_t p_n[2] = {0, 0};
+    uint32_t p_par = 0;    // bit x: parity of the next P of buffer x
     while (ok && sched.next(sg)) {
       const int n0 = uni(sg.nt[0]), n1 = uni(sg.nt[1]), n = max(n0, n1), nkeys = uni(sg.nkeys), kt0 = uni(sg.kt0);
       ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full, segs & 1, abort_flag, a.status, 621));
@@ -404,7 +404,8 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
         if (!ok) return;
         const int left = nkeys - (kt0 + t) * kFaKeys;   // keys of this tile (may exceed 128)
         const bool first = t < (NT == 2 ? 1 : 2);
-        const uint32_t par = p_n[x]++ & 1;
+        const uint32_t par = (p_par >> x) & 1;
+        p_par ^= 1u << x;
         {   // the V pieces and the first half of P
           const uint32_t pl = p + lane;
           const bool v = lane < VC;
@@ -451,42 +452,39 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
           if (rel) umma_commit(&bars->empty[(p + VC - 1) % NS]);
         }
       };
+      // One instance of each in the loop (the code has to stay in the instruction cache
+      // beside the softmax's): S of both buffers, then P.V and the next S in turn.
       if (NT == 2) {
-        auto kp = [&](int t) { return base + (uint32_t)t * (KC + VC); };
-        auto done_q = [&]() { if (ok && elect_one()) umma_commit(&bars->q_empty); };
-        qk(0, 0, kp(0), true, n1 == 0);
-        if (n == 1 && n1 == 0) done_q();
-        if (n1 > 0) {
-          qk(1, 1, kp(0), false, true);
-          if (n1 == 1) done_q();
-        }
-        for (int t = 0; t < n && ok; ++t) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int nx = x == 0 ? n0 : n1;
-            if (t >= nx) continue;
-            pv(x, t, kp(t) + KC, x == 0 || t >= n0, x == 1 || t >= n1);
-            if (t + 1 == nx && ok && elect_one()) umma_commit(&bars->o_full[x]);
-            if (t + 1 < nx) {
-              qk(x, x, kp(t + 1), x == 0 || t + 1 >= n0, x == 1 || t + 1 >= n1);
-              if (t + 2 == n && (x == 1 || n1 < n)) done_q();
-            }
+#pragma unroll 1
+        for (int i = 0; i < 2 * (n + 1) && ok; ++i) {
+          const int x = i & 1, t = i >> 1;
+          const int nx = x == 0 ? n0 : n1;
+          if (t > nx || nx == 0) continue;
+          const uint32_t p = base + (uint32_t)t * (KC + VC);
+          if (t > 0) {
+            pv(x, t - 1, p - VC, x == 0 || t > n0, x == 1 || t > n1);
+            if (t == nx && ok && elect_one()) umma_commit(&bars->o_full[x]);
+          }
+          if (t < nx) {
+            qk(x, x, p, x == 0 || t >= n0, x == 1 || t >= n1);
+            if (t + 1 == n && (x == 1 || n1 < n) && ok && elect_one()) umma_commit(&bars->q_empty);   // the last S
           }
         }
         base += (uint32_t)n * (KC + VC);
       } else {
         uint32_t p = base;
-        qk(0, 0, p, true, true);
-        p += KC;
-        for (int t = 0; t < n && ok; ++t) {
-          if (t + 1 < n) {
-            qk((t + 1) & 1, 0, p, true, true);
+#pragma unroll 1
+        for (int t = 0; t <= n && ok; ++t) {
+          if (t < n) {
+            qk(t & 1, 0, p, true, true);
             p += KC;
+            if (t + 1 == n && ok && elect_one()) umma_commit(&bars->q_empty);
           }
-          if ((t + 2 == n || n == 1) && ok && elect_one()) umma_commit(&bars->q_empty);   // the last S is on its way
-          pv(t & 1, t, p, true, true);
-          p += VC;
-          if (t + 2 >= n && ok && elect_one()) umma_commit(&bars->o_full[t & 1]);
+          if (t > 0) {
+            pv((t - 1) & 1, t - 1, p, true, true);
+            p += VC;
+            if (t + 1 >= n && ok && elect_one()) umma_commit(&bars->o_full[(t - 1) & 1]);
+          }
         }
         base = p;
       }
@@ -562,15 +560,15 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
               for (int c = 0; c < 32; ++c) s[32 * i + c] = (see >> c) & 1u ? s[32 * i + c] : -INFINITY;
             }
           }
-          float mx[4] = {fmaxf(s[0], s[4]), fmaxf(s[1], s[5]), fmaxf(s[2], s[6]), fmaxf(s[3], s[7])};
+          float mx[4] = {max_nan(s[0], s[4]), max_nan(s[1], s[5]), max_nan(s[2], s[6]), max_nan(s[3], s[7])};
 #pragma unroll
           for (int c = 8; c < 64; c += 8)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], fmaxf(s[c + i], s[c + 4 + i]));
-          float tmx = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          tmx = fmaxf(tmx, other(tmx));
+            for (int i = 0; i < 4; ++i) mx[i] = max_nan(mx[i], s[c + i], s[c + 4 + i]);
+          float tmx = max_nan(max_nan(mx[0], mx[1]), mx[2], mx[3]);
+          tmx = max_nan(tmx, other(tmx));
           float alpha = 1.f;
-          if (tmx > m + thr) {
+          if (!(tmx <= m + thr)) {                   // a NaN makes the whole row one
             alpha = ex2((m - tmx) * sc);             // 0 on a row's first visible keys
             m = tmx;
           }
