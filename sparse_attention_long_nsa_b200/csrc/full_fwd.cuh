@@ -23,7 +23,8 @@
 // sums by shuffles. With a thread to a whole row (8 warps) the kernel waited on its
 // own latencies: two warps a scheduler issued in 24% of the cycles.
 // K arrives in chunks of 128 keys x 64 channels and V in pieces of the
-// same 16 KB, through one ring in the order of use: the room that is left beside
+// same 16 KB, through one ring in the order of use (V of a tile and the next tile's
+// K make a group with one barrier): the room that is left beside
 // Q holds about one and a half tiles, and a common ring of small pieces keeps
 // more bytes in flight than separate rings of whole tiles would.
 //
@@ -55,8 +56,8 @@ struct FaShape {
 };
 
 struct FaBars {
-  uint64_t full[12], empty[12];
-  uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_full[2], drain, merge;   // p_full: keys 0-63, 64-127 of a tile
+  uint64_t full[16], empty[12];  // full: by group of pieces (at most 13 are under way); empty: by ring slot
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], drain, merge;
   uint32_t tmem_base;
   int abort;
 };
@@ -211,6 +212,7 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
   constexpr int NS = Sh::kSlots;
   constexpr int KC = DK / 64;               // ring pieces of a K tile
   constexpr int VC = DV / 64;               // ring pieces of a V tile: 64 keys x 128 or 128 keys x 64
+  constexpr int A = NT == 2 ? 1 : 2;        // S of tile t + A follows P.V of tile t
   constexpr uint32_t kColO = 256;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -223,16 +225,13 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&bars->full[i], 1);
-      mbar_init(&bars->empty[i], 1);
-    }
+    for (int i = 0; i < 16; ++i) mbar_init(&bars->full[i], 1);
+    for (int i = 0; i < NS; ++i) mbar_init(&bars->empty[i], 1);
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars->s_full[x], 1);
-      mbar_init(&bars->p_full[x][0], 256);
-      mbar_init(&bars->p_full[x][1], 256);
+      mbar_init(&bars->p_full[x], 256);
       mbar_init(&bars->o_full[x], 1);
     }
     mbar_init(&bars->drain, 1);
@@ -258,6 +257,7 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
       prefetch_tmap(&mp.v);
     }
     uint32_t pos = 0;      // ring pieces issued
+    uint32_t groups = 0;   // groups begun
     int q_n = 0;           // Q tiles issued
     int blk, brow = 0;     // page table cache: lane i holds the row of 64-key block blk + i
     while (ok && sched.next(sg)) {
@@ -292,69 +292,61 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
           r1 = r0 + 64;
         }
       };
-      auto acquire = [&]() -> uint32_t {
+      auto acquire = [&]() -> uint32_t {   // the next ring slot, free
         const uint32_t st = pos % NS;
         if (pos >= NS)
           ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->empty[st], ((pos / NS) - 1) & 1, abort_flag, a.status, 612));
-        ++pos;
+        if (ok) ++pos;
         return st;
       };
-      auto push_k = [&](int t) {
+      // group: V of tile tv (none when < 0) and K of tile tk (none when >= n)
+      auto push = [&](int tv, int tk) {
+        uint64_t* bar = &bars->full[groups & 15];
+        const bool v2 = tv >= 0 && (sg.kt0 + tv) * kFaKeys + 64 < sg.nkeys;   // the second 64 keys exist
+        const bool k2 = tk < n && (sg.kt0 + tk) * kFaKeys + 64 < sg.nkeys;
+        if (lane == 0)
+          mbar_arrive_expect_tx(bar, (tv < 0 ? 0u : (v2 ? 16384u : 8192u) * VC) + (tk >= n ? 0u : (k2 ? 16384u : 8192u) * KC));
+        ++groups;
         int r0, r1;
-        rows_of(t, r0, r1);
-        const bool two = (sg.kt0 + t) * kFaKeys + 64 < sg.nkeys;
+        if (tv >= 0) {
+          rows_of(tv, r0, r1);
 #pragma unroll
-        for (int c = 0; c < KC; ++c) {
-          const uint32_t st = acquire();
-          if (!ok) { --pos; return; }
-          if (lane == 0) {
-            uint8_t* dst = ring + st * kFaSlot;
-            mbar_arrive_expect_tx(&bars->full[st], two ? 16384u : 8192u);
-            tma_load_3d(dst, &mp.k, &bars->full[st], c * 64, sg.g, r0);
-            if (two) tma_load_3d(dst + 8192, &mp.k, &bars->full[st], c * 64, sg.g, r1);
+          for (int c = 0; c < VC; ++c) {
+            uint8_t* dst = ring + acquire() * kFaSlot;
+            if (!ok) return;
+            if (lane == 0) {
+              if (VC == 1) {          // 128 keys x 64 channels
+                tma_load_3d(dst, &mp.v, bar, 0, sg.g, r0);
+                if (v2) tma_load_3d(dst + 8192, &mp.v, bar, 0, sg.g, r1);
+              } else if (c == 0 || v2) {   // 64 keys x 128 channels
+                tma_load_3d(dst, &mp.v, bar, 0, sg.g, c == 0 ? r0 : r1);
+                tma_load_3d(dst + 8192, &mp.v, bar, 64, sg.g, c == 0 ? r0 : r1);
+              }
+            }
           }
         }
-      };
-      auto push_v = [&](int t) {
-        int r0, r1;
-        rows_of(t, r0, r1);
-        const bool two = (sg.kt0 + t) * kFaKeys + 64 < sg.nkeys;
+        if (tk < n) {
+          rows_of(tk, r0, r1);
 #pragma unroll
-        for (int c = 0; c < VC; ++c) {
-          const uint32_t st = acquire();
-          if (!ok) { --pos; return; }
-          if (lane == 0) {
-            uint8_t* dst = ring + st * kFaSlot;
-            if (VC == 1) {          // 128 keys x 64 channels
-              mbar_arrive_expect_tx(&bars->full[st], two ? 16384u : 8192u);
-              tma_load_3d(dst, &mp.v, &bars->full[st], 0, sg.g, r0);
-              if (two) tma_load_3d(dst + 8192, &mp.v, &bars->full[st], 0, sg.g, r1);
-            } else if (c == 0 || two) {   // 64 keys x 128 channels
-              mbar_arrive_expect_tx(&bars->full[st], 16384u);
-              tma_load_3d(dst, &mp.v, &bars->full[st], 0, sg.g, c == 0 ? r0 : r1);
-              tma_load_3d(dst + 8192, &mp.v, &bars->full[st], 64, sg.g, c == 0 ? r0 : r1);
-            } else {
-              mbar_arrive(&bars->full[st]);
+          for (int c = 0; c < KC; ++c) {
+            uint8_t* dst = ring + acquire() * kFaSlot;
+            if (!ok) return;
+            if (lane == 0) {
+              tma_load_3d(dst, &mp.k, bar, c * 64, sg.g, r0);
+              if (k2) tma_load_3d(dst + 8192, &mp.k, bar, c * 64, sg.g, r1);
             }
           }
         }
       };
-      if (NT == 2) {
-        for (int t = 0; t < n && ok; ++t) {
-          push_k(t);
-          if (ok) push_v(t);
-        }
-      } else {   // K of tile t + 1 before V of tile t
-        push_k(0);
-        for (int t = 0; t < n && ok; ++t) {
-          if (t + 1 < n) push_k(t + 1);
-          if (ok) push_v(t);
-        }
-      }
+#pragma unroll 1
+      for (int t = -A; t < n && ok; ++t)
+        if (t >= 0 || t + A < n) push(t < 0 ? -1 : t, t + A);
     }
     if (!ok && lane == 0) {   // let the copies still in flight land before the block exits
       if (q_n > 0) mbar_wait_drain(&bars->q_full, (q_n - 1) & 1);
-      for (uint32_t v = pos < NS ? 0 : pos - NS; v < pos; ++v) mbar_wait_drain(&bars->full[v % NS], (v / NS) & 1);
+      // (a group cut short by the abort never completes: its wait runs into its limit,
+      // by when its copies have landed)
+      for (uint32_t v = groups < 13 ? 0 : groups - 13; v < groups; ++v) mbar_wait_drain(&bars->full[v & 15], (v >> 4) & 1);
     }
   } else if (warp == 17) {
     // ------------------------------------------------------------ products
@@ -366,128 +358,104 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
     const uint64_t qdesc = umma_desc_sw128(q_a, 16, 1024);
     const uint64_t kdesc = umma_desc_sw128(ring_a, 16, 1024);
     const uint64_t vdesc = umma_desc_sw128(ring_a, 8192, 1024);
-    uint32_t base = 0;     // ring piece of the segment's first K chunk
-    int segs = 0;
+    uint32_t base = 0;     // ring piece after the last segment's
+    uint32_t groups = 0;   // groups waited for
+    uint32_t segs = 0;
     uint32_t p_par = 0;    // bit x: parity of the next P of buffer x
+    auto wait_group = [&]() -> bool {
+      const uint32_t gi = groups++;
+      return mbar_wait(&bars->full[gi & 15], (gi >> 4) & 1, abort_flag, a.status, 622);
+    };
+    // S of buffer x = Q (rows of half xq) . K at ring piece p; `rel`: its last use (one lane)
+    auto qk = [&](int x, int xq, uint32_t p, bool rel) {
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        const uint32_t st = (p + c) % NS;
+        const uint64_t qd = qdesc + (uint64_t)((xq * KC + c) * (16384 >> 4));
+        const uint64_t kd = kdesc + (uint64_t)(st * (kFaSlot >> 4));
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) umma_ss(tm + 128 * x, qd + kk * 2, kd + kk * 2, idesc_s, (c | kk) ? 1u : 0u);
+        if (rel) umma_commit(&bars->empty[st]);
+      }
+      umma_commit(&bars->s_full[x]);
+    };
     while (ok && sched.next(sg)) {
       const int n0 = uni(sg.nt[0]), n1 = uni(sg.nt[1]), n = max(n0, n1), nkeys = uni(sg.nkeys), kt0 = uni(sg.kt0);
       ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full, segs & 1, abort_flag, a.status, 621));
       if (!ok) break;
       ++segs;
-      tc_fence_after();
-      // S of buffer x = Q (rows of half xq) . K at ring piece p; `rel`: its last use;
-      // `fresh`: the pieces have not been waited for yet (all in one round, a lane each)
-      auto qk = [&](int x, int xq, uint32_t p, bool fresh, bool rel) {
-        if (!ok) return;
-        if (fresh) {
-          const uint32_t pl = p + lane;
-          ok = __all_sync(0xffffffffu, lane >= KC || mbar_wait(&bars->full[pl % NS], (pl / NS) & 1, abort_flag, a.status, 622));
-          if (!ok) return;
-        }
+      // the first S of each buffer
+#pragma unroll 1
+      for (int x = 0; x < 2 && ok; ++x) {
+        if (NT == 2 ? (x == 1 && n1 == 0) : x >= n) continue;
+        if (NT == 1 || x == 0) ok = __all_sync(0xffffffffu, wait_group());
+        if (!ok) break;
         if (elect_one()) {
           tc_fence_after();
+          qk(x, NT == 2 ? x : 0, base + (NT == 2 ? 0 : x * KC), NT == 1 || x == 1 || n1 == 0);
+          if (NT == 1 ? n <= 2 && x == n - 1 : n == 1 && (x == 1 || n1 == 0)) umma_commit(&bars->q_empty);
+        }
+        __syncwarp();
+      }
+      uint32_t p = base + (NT == 2 ? 1 : min(n, 2)) * KC;   // V of tile t, then K of tile t + A
+      // One instance of the step in the loop: its code has to stay in the instruction
+      // cache beside the softmax's. All that a step needs is waited for at once, while
+      // the products before it are still in the tensor core's queue.
+#pragma unroll 1
+      for (int i = 0; i < (NT == 2 ? 2 * n : n) && ok; ++i) {
+        const int x = i & 1, t = NT == 2 ? i >> 1 : i;
+        const int nx = NT == 1 ? n : x == 0 ? n0 : n1;      // tiles of this buffer (NT = 1: of both)
+        const bool fresh = NT == 1 || x == 0 || t >= n0;    // first use of the group
+        const bool last = NT == 1 || x == 1 || t >= n1;     // last use of V
+        if (t < nx) {
+          ok = __all_sync(0xffffffffu, (!fresh || wait_group()) &&
+                                           mbar_wait(&bars->p_full[x], (p_par >> x) & 1, abort_flag, a.status, 624));
+          p_par ^= 1u << x;
+          if (!ok) break;
+          const int left = nkeys - (kt0 + t) * kFaKeys;     // keys of this tile (may exceed 128)
+          if (left < kFaKeys && fresh) {                    // clear the V rows past the last key
 #pragma unroll
-          for (int c = 0; c < KC; ++c) {
-            const uint32_t st = (p + c) % NS;
-            const uint64_t qd = qdesc + (uint64_t)((xq * KC + c) * (16384 >> 4));
-            const uint64_t kd = kdesc + (uint64_t)(st * (kFaSlot >> 4));
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_ss(tm + 128 * x, qd + kk * 2, kd + kk * 2, idesc_s, (c | kk) ? 1u : 0u);
-            if (rel) umma_commit(&bars->empty[st]);
+            for (int c = 0; c < VC; ++c) {
+              const int have = left - c * 64;
+              const int rows = VC == 1 && have > 64 ? 128 : 64;   // rows loaded
+              uint8_t* vs = ring + (p + c) % NS * kFaSlot;
+              if (have > 0 && have < rows)
+                for (int k = have * 8 + lane; k < rows * 8; k += 32) {
+                  *reinterpret_cast<uint4*>(vs + k * 16) = make_uint4(0, 0, 0, 0);
+                  if (VC == 2) *reinterpret_cast<uint4*>(vs + 8192 + k * 16) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
           }
-          umma_commit(&bars->s_full[x]);
-        }
-      };
-      // O of buffer x (+)= P . V of tile t at ring piece p
-      auto pv = [&](int x, int t, uint32_t p, bool fresh, bool rel) {
-        if (!ok) return;
-        const int left = nkeys - (kt0 + t) * kFaKeys;   // keys of this tile (may exceed 128)
-        const bool first = t < (NT == 2 ? 1 : 2);
-        const uint32_t par = (p_par >> x) & 1;
-        p_par ^= 1u << x;
-        {   // the V pieces and the first half of P
-          const uint32_t pl = p + lane;
-          const bool v = lane < VC;
-          ok = __all_sync(0xffffffffu, (v ? !fresh : lane != 31) ||
-                                           mbar_wait(v ? &bars->full[pl % NS] : &bars->p_full[x][0],
-                                                     v ? (pl / NS) & 1 : par, abort_flag, a.status, 624));
-          if (!ok) return;
-        }
-        constexpr int kPer = VC == 1 ? 128 : 64;        // keys of a piece
-        if (left < kFaKeys && fresh) {                  // clear the rows past the last key
+          if (elect_one()) {
+            tc_fence_after();
+            // O (+)= P . V, keys 64 h .. + 63: piece h (VC = 2) or rows 64 h of the one piece
 #pragma unroll
-          for (int c = 0; c < VC; ++c) {
-            const int have = left - c * 64;
-            const int rows = VC == 1 && have <= 64 ? 64 : kPer;   // rows loaded
-            uint8_t* vs = ring + (p + c) % NS * kFaSlot;
-            if (have > 0 && have < rows)
-              for (int i = have * 8 + lane; i < rows * 8; i += 32) {
-                *reinterpret_cast<uint4*>(vs + i * 16) = make_uint4(0, 0, 0, 0);
-                if (VC == 2) *reinterpret_cast<uint4*>(vs + 8192 + i * 16) = make_uint4(0, 0, 0, 0);
+            for (int h = 0; h < 2; ++h) {
+              const uint64_t vd = vdesc + (uint64_t)((p + (VC == 2 ? h : 0)) % NS * (kFaSlot >> 4)) +
+                                  (VC == 1 ? (uint64_t)(h * (8192 >> 4)) : 0);
+              if (h == 0 || left > 64) {                    // else no keys there: V was not loaded
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_ts(tm + kColO + 128 * x, tm + 128 * x + (h * 4 + kk) * 8, vd + kk * (2048 >> 4), idesc_o,
+                          (t < A && h == 0 && kk == 0) ? 0u : 1u);
               }
+              if (last && (VC == 2 || h == 1)) umma_commit(&bars->empty[(p + (VC == 2 ? h : 0)) % NS]);
+            }
+            if (t + A < nx) {
+              const bool last_k = NT == 1 || x == 1 || t + A >= n1;
+              qk(x, NT == 2 ? x : 0, p + VC, last_k);
+              if (t + A + 1 == n && last_k) umma_commit(&bars->q_empty);   // the last S is on its way
+            } else {
+              umma_commit(&bars->o_full[x]);
+            }
           }
-          fence_proxy_async_smem();
           __syncwarp();
         }
-        // keys 64 h .. + 63: piece h (VC = 2) or rows 64 h of the one piece
-        auto half = [&](int h) {
-          const uint64_t vd = vdesc + (uint64_t)((p + (VC == 2 ? h : 0)) % NS * (kFaSlot >> 4)) +
-                              (VC == 1 ? (uint64_t)(h * (8192 >> 4)) : 0);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_ts(tm + kColO + 128 * x, tm + 128 * x + (h * 4 + kk) * 8, vd + kk * (2048 >> 4), idesc_o,
-                    (first && h == 0 && kk == 0) ? 0u : 1u);
-        };
-        if (elect_one()) {
-          tc_fence_after();
-          half(0);
-          if (VC == 2 && rel) umma_commit(&bars->empty[p % NS]);
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->p_full[x][1], par, abort_flag, a.status, 623));
-        if (!ok) return;
-        if (elect_one()) {
-          tc_fence_after();
-          if (left > 64) half(1);                       // no keys there: V was not loaded
-          if (rel) umma_commit(&bars->empty[(p + VC - 1) % NS]);
-        }
-      };
-      // One instance of each in the loop (the code has to stay in the instruction cache
-      // beside the softmax's): S of both buffers, then P.V and the next S in turn.
-      if (NT == 2) {
-#pragma unroll 1
-        for (int i = 0; i < 2 * (n + 1) && ok; ++i) {
-          const int x = i & 1, t = i >> 1;
-          const int nx = x == 0 ? n0 : n1;
-          if (t > nx || nx == 0) continue;
-          const uint32_t p = base + (uint32_t)t * (KC + VC);
-          if (t > 0) {
-            pv(x, t - 1, p - VC, x == 0 || t > n0, x == 1 || t > n1);
-            if (t == nx && ok && elect_one()) umma_commit(&bars->o_full[x]);
-          }
-          if (t < nx) {
-            qk(x, x, p, x == 0 || t >= n0, x == 1 || t >= n1);
-            if (t + 1 == n && (x == 1 || n1 < n) && ok && elect_one()) umma_commit(&bars->q_empty);   // the last S
-          }
-        }
-        base += (uint32_t)n * (KC + VC);
-      } else {
-        uint32_t p = base;
-#pragma unroll 1
-        for (int t = 0; t <= n && ok; ++t) {
-          if (t < n) {
-            qk(t & 1, 0, p, true, true);
-            p += KC;
-            if (t + 1 == n && ok && elect_one()) umma_commit(&bars->q_empty);
-          }
-          if (t > 0) {
-            pv((t - 1) & 1, t - 1, p, true, true);
-            p += VC;
-            if (t + 1 >= n && ok && elect_one()) umma_commit(&bars->o_full[(t - 1) & 1]);
-          }
-        }
-        base = p;
+        if (NT == 1 || x == 1) p += VC + (t + A < n ? KC : 0);
       }
+      base = p;
     }
     // every product has finished before tensor memory is released
     if (elect_one()) {
@@ -601,17 +569,13 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
               w[c >> 1] = pack_bf16x2(p.x, p.y);
             }
             tmem_st16_h<16>(s_col + 32 * i, w);
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&bars->p_full[x][i]);        // the product may start on the first 64 keys
           }
           const float2 sm = add2(sum[0], sum[1]);
           l += sm.x + sm.y;
-        } else {
-          tc_fence_before();
-          mbar_arrive(&bars->p_full[x][0]);
-          mbar_arrive(&bars->p_full[x][1]);
+          tmem_st_wait();
         }
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[x]);
         any = true;
       }
       if (!ok) break;
