@@ -31,18 +31,21 @@ namespace {
 constexpr int kThreads = 384;   // 8 warps of elementwise work, loads, products, row values, one idle
 constexpr int kPiece = 16384;   // 128 rows x 64 channels, 128-byte swizzled
 constexpr int kRows = 128;
-constexpr int kMaxSlots = 10;
 
-__host__ __device__ constexpr int ring_slots(int dk, int dv) {
-  const int n = (232448 - 1024 - (dk + dv) * 256 - 4096) / kPiece;
-  return n > kMaxSlots ? kMaxSlots : n;
+// Streamed operands: two stages of the d_k wide one, and of the d_v wide one as many
+// as fit beside them and the resident tiles (one at 192 + 128: its next tile is
+// loaded while the two products after its last use run). A stage's pieces are
+// adjacent, so that it is one operand of 64, 128 or 192 columns: products of 64
+// columns that take their other operand from tensor memory run at half the rate.
+__host__ __device__ constexpr int wide_stages(int dk, int dv) {
+  return (232448 - 1024 - 4096 - (dk + dv) * 256 - 2 * dk * 256) / (dv * 256) >= 2 ? 2 : 1;
 }
 __host__ __device__ constexpr int bwd_smem(int dk, int dv) {
-  return 1024 + (dk + dv) * 256 + ring_slots(dk, dv) * kPiece + 4096;
+  return 1024 + (dk + dv) * 256 + 2 * dk * 256 + wide_stages(dk, dv) * dv * 256 + 4096;
 }
 
 struct BwdBars {
-  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];   // stages of the d_k / d_v wide operand
   uint64_t fix_full, fix_empty;               // the block's resident operands
   uint64_t s_full, s_read, p_full, dp_full, dp_read, ds_full, ds_free, acc_full, drain;
   uint64_t row_full[2], row_empty[2];
@@ -55,20 +58,12 @@ __device__ __forceinline__ void clear_rows(uint8_t* piece, int from, int lane) {
   for (int i = from * 8 + lane; i < kRows * 8; i += 32) *reinterpret_cast<uint4*>(piece + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
-// ring cursor of one role
-template <int NS>
-struct Ring {
-  BwdBars* bars;
-  volatile int* abort_flag;
-  uint32_t* status;
-  uint32_t pos = 0;
-  __device__ bool wait_full(uint32_t p, uint32_t site) const {
-    return __all_sync(0xffffffffu, mbar_wait(&bars->full[p % NS], (p / NS) & 1, abort_flag, status, site));
-  }
-  __device__ bool wait_empty(uint32_t p, uint32_t site) const {
-    return p < NS || __all_sync(0xffffffffu, mbar_wait(&bars->empty[p % NS], ((p / NS) - 1) & 1, abort_flag, status, site));
-  }
-};
+// one lane waits for the copies in flight before its block exits
+__device__ __forceinline__ void drain_loads(BwdBars* bars, int segs, uint32_t k_n, uint32_t v_n, uint32_t vs) {
+  if (segs > 0) mbar_wait_drain(&bars->fix_full, (segs - 1) & 1);
+  for (uint32_t i = k_n < 2 ? 0 : k_n - 2; i < k_n; ++i) mbar_wait_drain(&bars->k_full[i & 1], (i >> 1) & 1);
+  for (uint32_t i = v_n < vs ? 0 : v_n - vs; i < v_n; ++i) mbar_wait_drain(&bars->v_full[i % vs], (i / vs) & 1);
+}
 
 // dO o O summed over a row, beside the row's lse in log2 units: 8 channels a lane
 template <int DV>
@@ -161,10 +156,12 @@ struct KvSched {
   }
 };
 
-__device__ __forceinline__ void bwd_init(BwdBars* bars, int ns) {
-  for (int i = 0; i < ns; ++i) {
-    mbar_init(&bars->full[i], 1);
-    mbar_init(&bars->empty[i], 1);
+__device__ __forceinline__ void bwd_init(BwdBars* bars) {
+  for (int i = 0; i < 2; ++i) {
+    mbar_init(&bars->k_full[i], 1);
+    mbar_init(&bars->k_empty[i], 1);
+    mbar_init(&bars->v_full[i], 1);
+    mbar_init(&bars->v_empty[i], 1);
   }
   mbar_init(&bars->fix_full, 1);
   mbar_init(&bars->fix_empty, 1);
@@ -195,18 +192,20 @@ __device__ __forceinline__ uint4 pack_out(const float* v, float f) {
 template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const FullBwdArgs a,
                                                                       const __grid_constant__ FullBwdMaps mp) {
-  constexpr int KC = DK / 64, VC = DV / 64, NS = ring_slots(DK, DV);
+  constexpr int KC = DK / 64, VC = DV / 64, VS = wide_stages(DK, DV);
+  constexpr int kKStage = KC * kPiece, kVStage = VC * kPiece;
   constexpr uint32_t kColDP = 64, kColDV = 192, kColDK = 320;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* Ks = smem;                       // K pieces, then V pieces
   uint8_t* Vs = Ks + KC * kPiece;
-  uint8_t* ring = Vs + VC * kPiece;
-  float2* rowv = reinterpret_cast<float2*>(ring + NS * kPiece);   // [2][128] (lse, delta) of the row tile
+  uint8_t* Qr = Vs + kVStage;               // streamed Q, dO
+  uint8_t* Gr = Qr + 2 * kKStage;
+  float2* rowv = reinterpret_cast<float2*>(Gr + VS * kVStage);    // [2][128] (lse, delta) of the row tile
   BwdBars* bars = reinterpret_cast<BwdBars*>(rowv + 2 * kRows);
   volatile int* abort_flag = &bars->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) bwd_init(bars, NS);
+  if (tid == 0) bwd_init(bars);
   if (warp == 0) tmem_alloc(&bars->tmem_base, 512);
   tc_fence_before();
   __syncthreads();
@@ -222,7 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
 
   if (warp == 8) {
     // ------------------------------------------------------------ loads
-    Ring<NS> rg{bars, abort_flag, a.status};
+    uint32_t k_n = 0, v_n = 0;   // stages filled
+    uint32_t tiles = 0;
     int segs = 0;
     while (ok && sched.next(sg)) {
       if (segs > 0) ok = uwait(&bars->fix_empty, segs - 1, 641);
@@ -234,120 +234,114 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
         for (int c = 0; c < VC; ++c) tma_load_3d(Vs + c * kPiece, &mp.v, &bars->fix_full, c * 64, sg.g, row);
       }
       ++segs;
-      for (int j = 0; j < sg.n && ok; ++j) {
+      for (int j = 0; j < sg.n && ok; ++j, ++tiles) {
         const int row = (int)(sg.tok0 + (int64_t)(sg.r0 + j) * TOK);
-        for (int c = 0; c < VC + KC && ok; ++c) {   // dO before Q
-          ok = rg.wait_empty(rg.pos, 642);
-          if (!ok) break;
-          if (lane == 0) {
-            const uint32_t st = rg.pos % NS;
-            mbar_arrive_expect_tx(&bars->full[st], kPiece);
-            if (c < VC) tma_load_3d(ring + st * kPiece, &mp.dout, &bars->full[st], c * 64, sg.g * a.G, row);
-            else tma_load_3d(ring + st * kPiece, &mp.q, &bars->full[st], (c - VC) * 64, sg.g * a.G, row);
-          }
-          ++rg.pos;
+        const uint32_t ks = tiles & 1, vs = tiles % VS;
+        if (tiles >= 2) ok = uwait(&bars->k_empty[ks], (tiles >> 1) - 1, 642);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->k_full[ks], kKStage);
+          for (int c = 0; c < KC; ++c)
+            tma_load_3d(Qr + ks * kKStage + c * kPiece, &mp.q, &bars->k_full[ks], c * 64, sg.g * a.G, row);
         }
+        ++k_n;
+        if (tiles >= VS) ok = uwait(&bars->v_empty[vs], tiles / VS - 1, 643);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->v_full[vs], kVStage);
+          for (int c = 0; c < VC; ++c)
+            tma_load_3d(Gr + vs * kVStage + c * kPiece, &mp.dout, &bars->v_full[vs], c * 64, sg.g * a.G, row);
+        }
+        ++v_n;
       }
     }
-    if (!ok && lane == 0) {   // copies in flight land before the block exits
-      if (segs > 0) mbar_wait_drain(&bars->fix_full, (segs - 1) & 1);
-      for (uint32_t v = rg.pos < NS ? 0 : rg.pos - NS; v < rg.pos; ++v)
-        mbar_wait_drain(&bars->full[v % NS], (v / NS) & 1);
-    }
+    if (!ok && lane == 0) drain_loads(bars, segs, k_n, v_n, VS);
   } else if (warp == 9) {
     // ------------------------------------------------------------ products
+    // (operands uniform over the warp, see the forward kernel)
+    const uint32_t tm = uni(tmem);
     const uint32_t id_s = umma_idesc_bf16(128, 128, false, false);
-    const uint32_t id_g = umma_idesc_bf16(128, 64, false, true);
-    const uint64_t kd = umma_desc_sw128(smem_u32(Ks), 16, 1024), vd = umma_desc_sw128(smem_u32(Vs), 16, 1024);
-    const uint64_t rd = umma_desc_sw128(smem_u32(ring), 16, 1024);      // rows x channels, K-major
-    Ring<NS> rg{bars, abort_flag, a.status};
+    const uint32_t id_v = umma_idesc_bf16(128, DV, false, true), id_k = umma_idesc_bf16(128, DK, false, true);
+    const uint64_t kd = umma_desc_sw128(uni(smem_u32(Ks)), 16, 1024), vd = umma_desc_sw128(uni(smem_u32(Vs)), 16, 1024);
+    const uint32_t q_a = uni(smem_u32(Qr)), g_a = uni(smem_u32(Gr));
+    const uint64_t qs = umma_desc_sw128(q_a, 16, 1024), gs = umma_desc_sw128(g_a, 16, 1024);             // rows x channels
+    const uint64_t qt = umma_desc_sw128(q_a, kPiece, 1024), gt = umma_desc_sw128(g_a, kPiece, 1024);     // channels x rows
     uint32_t tiles = 0;
     int segs = 0;
     while (ok && sched.next(sg)) {
+      const int n = uni(sg.n), L = uni(sg.L), r0 = uni(sg.r0);
       ok = uwait(&bars->fix_full, segs, 651);
       if (!ok) break;
       ++segs;
-      for (int j = 0; j < sg.n && ok; ++j, ++tiles) {
-        const uint32_t pd = rg.pos, pq = rg.pos + VC;   // ring pieces of dO and Q
-        const int left = min(sg.L - (sg.r0 + j) * TOK, TOK) * a.G;   // rows of the tile that exist
+#pragma unroll 1
+      for (int j = 0; j < n && ok; ++j, ++tiles) {
+        const uint32_t ks = tiles & 1, vs = tiles % VS;
+        const int left = min(L - (r0 + j) * TOK, TOK) * a.G;   // rows of the tile that exist
         // S^T = K Q^T over the P and dS that the products before it have read
-        for (int c = 0; c < KC && ok; ++c) {
-          ok = rg.wait_full(pq + c, 652);
-          if (!ok) break;
-          uint8_t* piece = ring + (pq + c) % NS * kPiece;
-          if (left < kRows) {
-            clear_rows(piece, left, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (lane == 0) {
-            tc_fence_after();
-            const uint64_t q = rd + (uint64_t)((pq + c) % NS * (kPiece >> 4));
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_ss(tmem, kd + (uint64_t)(c * (kPiece >> 4) + kk * 2), q + kk * 2, id_s, (c | kk) ? 1u : 0u);
-          }
-        }
+        ok = uwait(&bars->k_full[ks], tiles >> 1, 652);
         if (!ok) break;
-        if (lane == 0) umma_commit(&bars->s_full);
-        // dP^T = V dO^T beside P: the upper columns of S^T have to be read
-        for (int c = 0; c < VC && ok; ++c) {
-          ok = rg.wait_full(pd + c, 653);
-          if (!ok) break;
-          if (left < kRows) {
-            clear_rows(ring + (pd + c) % NS * kPiece, left, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
+        if (left < kRows) {
+          for (int c = 0; c < KC; ++c) clear_rows(Qr + ks * kKStage + c * kPiece, left, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
         }
-        ok = ok && uwait(&bars->s_read, tiles, 654);
-        if (!ok) break;
-        if (lane == 0) {
+        if (elect_one()) {
           tc_fence_after();
+          const uint64_t q = qs + (uint64_t)(ks * (kKStage >> 4));
 #pragma unroll
-          for (int c = 0; c < VC; ++c) {
-            const uint64_t d = rd + (uint64_t)((pd + c) % NS * (kPiece >> 4));
+          for (int kk = 0; kk < KC * 4; ++kk) {
+            const uint64_t o = (uint64_t)((kk >> 2) * (kPiece >> 4) + (kk & 3) * 2);
+            umma_ss(tm, kd + o, q + o, id_s, kk ? 1u : 0u);
+          }
+          umma_commit(&bars->s_full);
+        }
+        // dP^T = V dO^T beside P: the upper columns of S^T have to be read
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[vs], (tiles / VS) & 1, abort_flag, a.status, 653) &&
+                                         mbar_wait(&bars->s_read, tiles & 1, abort_flag, a.status, 654));
+        if (!ok) break;
+        if (left < kRows) {
+          for (int c = 0; c < VC; ++c) clear_rows(Gr + vs * kVStage + c * kPiece, left, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (elect_one()) {
+          tc_fence_after();
+          const uint64_t g = gs + (uint64_t)(vs * (kVStage >> 4));
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_ss(tmem + kColDP, vd + (uint64_t)(c * (kPiece >> 4) + kk * 2), d + kk * 2, id_s, (c | kk) ? 1u : 0u);
+          for (int kk = 0; kk < VC * 4; ++kk) {
+            const uint64_t o = (uint64_t)((kk >> 2) * (kPiece >> 4) + (kk & 3) * 2);
+            umma_ss(tm + kColDP, vd + o, g + o, id_s, kk ? 1u : 0u);
           }
           umma_commit(&bars->dp_full);
-          if (j + 1 == sg.n) umma_commit(&bars->fix_empty);
+          if (j + 1 == n) umma_commit(&bars->fix_empty);
         }
         // dV += P^T dO
         ok = uwait(&bars->p_full, tiles, 655);
         if (!ok) break;
-        if (lane == 0) {
+        if (elect_one()) {
           tc_fence_after();
+          const uint64_t g = gt + (uint64_t)(vs * (kVStage >> 4));
 #pragma unroll
-          for (int c = 0; c < VC; ++c) {
-            const uint64_t d = rd + (uint64_t)((pd + c) % NS * (kPiece >> 4));
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_ts(tmem + kColDV + 64 * c, tmem + kk * 8, d + (uint64_t)(kk * (2048 >> 4)), id_g, (j | kk) ? 1u : 0u);
-            umma_commit(&bars->empty[(pd + c) % NS]);
-          }
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts(tm + kColDV, tm + kk * 8, g + (uint64_t)(kk * (2048 >> 4)), id_v, (j | kk) ? 1u : 0u);
+          umma_commit(&bars->v_empty[vs]);
         }
         // dK += dS^T Q
         ok = uwait(&bars->ds_full, tiles, 656);
         if (!ok) break;
-        if (lane == 0) {
+        if (elect_one()) {
           tc_fence_after();
+          const uint64_t q = qt + (uint64_t)(ks * (kKStage >> 4));
 #pragma unroll
-          for (int c = 0; c < KC; ++c) {
-            const uint64_t q = rd + (uint64_t)((pq + c) % NS * (kPiece >> 4));
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_ts(tmem + kColDK + 64 * c, tmem + kColDP + kk * 8, q + (uint64_t)(kk * (2048 >> 4)), id_g,
-                      (j | kk) ? 1u : 0u);
-            umma_commit(&bars->empty[(pq + c) % NS]);
-          }
-          if (j + 1 == sg.n) umma_commit(&bars->acc_full);
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts(tm + kColDK, tm + kColDP + kk * 8, q + (uint64_t)(kk * (2048 >> 4)), id_k, (j | kk) ? 1u : 0u);
+          umma_commit(&bars->k_empty[ks]);
+          if (j + 1 == n) umma_commit(&bars->acc_full);
         }
-        rg.pos += VC + KC;
+        __syncwarp();
       }
     }
-    if (lane == 0) {   // every product has finished before tensor memory is released
+    if (elect_one()) {   // every product has finished before tensor memory is released
       umma_commit(&bars->drain);
       mbar_wait_drain(&bars->drain, 0);
     }
@@ -538,17 +532,19 @@ __global__ void __launch_bounds__(256) nsa_full_bwd_merge_kernel(const FullBwdAr
 template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_q_kernel(const FullBwdArgs a,
                                                                      const __grid_constant__ FullBwdMaps mp) {
-  constexpr int KC = DK / 64, VC = DV / 64, NS = ring_slots(DK, DV);
+  constexpr int KC = DK / 64, VC = DV / 64, VS = wide_stages(DK, DV);
+  constexpr int kKStage = KC * kPiece, kVStage = VC * kPiece;
   constexpr uint32_t kColDP = 128, kColDQ = 256, kColDS = 448;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* Qs = smem;                       // Q pieces, then dO pieces
   uint8_t* Gs = Qs + KC * kPiece;
-  uint8_t* ring = Gs + VC * kPiece;
-  BwdBars* bars = reinterpret_cast<BwdBars*>(ring + NS * kPiece);
+  uint8_t* Kr = Gs + kVStage;               // streamed K, V
+  uint8_t* Vr = Kr + 2 * kKStage;
+  BwdBars* bars = reinterpret_cast<BwdBars*>(Vr + VS * kVStage);
   volatile int* abort_flag = &bars->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) bwd_init(bars, NS);
+  if (tid == 0) bwd_init(bars);
   if (warp == 0) tmem_alloc(&bars->tmem_base, 512);
   tc_fence_before();
   __syncthreads();
@@ -586,7 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_q_kernel(const FullB
 
   if (warp == 8) {
     // ------------------------------------------------------------ loads
-    Ring<NS> rg{bars, abort_flag, a.status};
+    uint32_t k_n = 0, v_n = 0;   // stages filled
+    uint32_t tiles = 0;
     int segs = 0;
     while (ok && next()) {
       if (segs > 0) ok = uwait(&bars->fix_empty, segs - 1, 681);
@@ -598,110 +595,107 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_q_kernel(const FullB
         for (int c = 0; c < VC; ++c) tma_load_3d(Gs + c * kPiece, &mp.dout, &bars->fix_full, c * 64, g * a.G, row);
       }
       ++segs;
-      for (int j = 0; j < nkt && ok; ++j) {
+      for (int j = 0; j < nkt && ok; ++j, ++tiles) {
         const int row = (int)(tok0 + (int64_t)j * kRows);
-        for (int c = 0; c < VC + KC && ok; ++c) {   // V before K
-          ok = rg.wait_empty(rg.pos, 682);
-          if (!ok) break;
-          if (lane == 0) {
-            const uint32_t st = rg.pos % NS;
-            mbar_arrive_expect_tx(&bars->full[st], kPiece);
-            if (c < VC) tma_load_3d(ring + st * kPiece, &mp.v, &bars->full[st], c * 64, g, row);
-            else tma_load_3d(ring + st * kPiece, &mp.k, &bars->full[st], (c - VC) * 64, g, row);
-          }
-          ++rg.pos;
+        const uint32_t ks = tiles & 1, vs = tiles % VS;
+        if (tiles >= VS) ok = uwait(&bars->v_empty[vs], tiles / VS - 1, 683);   // V is free before K
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->v_full[vs], kVStage);
+          for (int c = 0; c < VC; ++c)
+            tma_load_3d(Vr + vs * kVStage + c * kPiece, &mp.v, &bars->v_full[vs], c * 64, g, row);
         }
+        ++v_n;
+        if (tiles >= 2) ok = uwait(&bars->k_empty[ks], (tiles >> 1) - 1, 682);
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars->k_full[ks], kKStage);
+          for (int c = 0; c < KC; ++c)
+            tma_load_3d(Kr + ks * kKStage + c * kPiece, &mp.k, &bars->k_full[ks], c * 64, g, row);
+        }
+        ++k_n;
       }
     }
-    if (!ok && lane == 0) {
-      if (segs > 0) mbar_wait_drain(&bars->fix_full, (segs - 1) & 1);
-      for (uint32_t v = rg.pos < NS ? 0 : rg.pos - NS; v < rg.pos; ++v)
-        mbar_wait_drain(&bars->full[v % NS], (v / NS) & 1);
-    }
+    if (!ok && lane == 0) drain_loads(bars, segs, k_n, v_n, VS);
   } else if (warp == 9) {
     // ------------------------------------------------------------ products
-    // S and dP of tile j + 1 are issued before dQ of tile j: the ring holds
-    // K(j), V(j + 1) and K(j + 1) at once (V(j) is released by its dP)
-    const uint32_t id_s = umma_idesc_bf16(128, 128, false, false);
-    const uint32_t id_g = umma_idesc_bf16(128, 64, false, true);
-    const uint64_t qd = umma_desc_sw128(smem_u32(Qs), 16, 1024), gd = umma_desc_sw128(smem_u32(Gs), 16, 1024);
-    const uint64_t rd = umma_desc_sw128(smem_u32(ring), 16, 1024);
-    Ring<NS> rg{bars, abort_flag, a.status};
-    uint32_t tiles = 0, done = 0;   // S / dP issued; dQ issued
+    // S and dP of tile j + 1 are issued before dQ of tile j: both stages of K are in
+    // use then, V(j) is released by its dP
+    const uint32_t tm = uni(tmem);
+    const uint32_t id_s = umma_idesc_bf16(128, 128, false, false), id_k = umma_idesc_bf16(128, DK, false, true);
+    const uint64_t qd = umma_desc_sw128(uni(smem_u32(Qs)), 16, 1024), gd = umma_desc_sw128(uni(smem_u32(Gs)), 16, 1024);
+    const uint32_t k_a = uni(smem_u32(Kr)), v_a = uni(smem_u32(Vr));
+    const uint64_t kd = umma_desc_sw128(k_a, 16, 1024), vd = umma_desc_sw128(v_a, 16, 1024);
+    const uint64_t kt = umma_desc_sw128(k_a, kPiece, 1024);   // channels x keys
+    uint32_t tiles = 0;    // S issued
     int segs = 0;
     while (ok && next()) {
+      const int n = uni(nkt), keys = uni(min(i0 + TOK, L));
       ok = uwait(&bars->fix_full, segs, 691);
       if (!ok) break;
       ++segs;
-      const uint32_t base = rg.pos;
-      auto scores = [&](int j) {
-        const uint32_t pv = base + (uint32_t)j * (VC + KC), pk = pv + VC;
-        const int left = min(i0 + TOK, L) - j * kRows;   // keys in sight
-        if (tiles > 0) ok = uwait(&bars->s_read, tiles - 1, 692);
-        for (int c = 0; c < KC && ok; ++c) {
-          ok = rg.wait_full(pk + c, 693);
+      // step j: S and dP of tile j, then dQ of tile j - 1
+#pragma unroll 1
+      for (int j = 0; j <= n && ok; ++j) {
+        if (j < n) {
+          const uint32_t ks = tiles & 1, vs = tiles % VS;
+          const int left = keys - j * kRows;   // keys in sight
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(&bars->k_full[ks], (tiles >> 1) & 1, abort_flag, a.status, 693) &&
+                              (tiles == 0 || mbar_wait(&bars->s_read, (tiles - 1) & 1, abort_flag, a.status, 692)));
           if (!ok) break;
           if (left < kRows) {   // dS is zero there, but 0 x NaN is not
-            clear_rows(ring + (pk + c) % NS * kPiece, left, lane);
+            for (int c = 0; c < KC; ++c) clear_rows(Kr + ks * kKStage + c * kPiece, left, lane);
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (lane == 0) {
+          if (elect_one()) {
             tc_fence_after();
-            const uint64_t k = rd + (uint64_t)((pk + c) % NS * (kPiece >> 4));
+            const uint64_t k = kd + (uint64_t)(ks * (kKStage >> 4));
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_ss(tmem, qd + (uint64_t)(c * (kPiece >> 4) + kk * 2), k + kk * 2, id_s, (c | kk) ? 1u : 0u);
+            for (int kk = 0; kk < KC * 4; ++kk) {
+              const uint64_t o = (uint64_t)((kk >> 2) * (kPiece >> 4) + (kk & 3) * 2);
+              umma_ss(tm, qd + o, k + o, id_s, kk ? 1u : 0u);
+            }
+            umma_commit(&bars->s_full);
           }
-        }
-        if (!ok) return;
-        if (lane == 0) umma_commit(&bars->s_full);
-        if (tiles > 0) ok = uwait(&bars->dp_read, tiles - 1, 694);
-        for (int c = 0; c < VC && ok; ++c) {
-          ok = rg.wait_full(pv + c, 695);
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(&bars->v_full[vs], (tiles / VS) & 1, abort_flag, a.status, 695) &&
+                              (tiles == 0 || mbar_wait(&bars->dp_read, (tiles - 1) & 1, abort_flag, a.status, 694)));
           if (!ok) break;
-          if (lane == 0) {
+          if (elect_one()) {
             tc_fence_after();
-            const uint64_t v = rd + (uint64_t)((pv + c) % NS * (kPiece >> 4));
+            const uint64_t v = vd + (uint64_t)(vs * (kVStage >> 4));
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_ss(tmem + kColDP, gd + (uint64_t)(c * (kPiece >> 4) + kk * 2), v + kk * 2, id_s, (c | kk) ? 1u : 0u);
-            umma_commit(&bars->empty[(pv + c) % NS]);
+            for (int kk = 0; kk < VC * 4; ++kk) {
+              const uint64_t o = (uint64_t)((kk >> 2) * (kPiece >> 4) + (kk & 3) * 2);
+              umma_ss(tm + kColDP, gd + o, v + o, id_s, kk ? 1u : 0u);
+            }
+            umma_commit(&bars->v_empty[vs]);
+            umma_commit(&bars->dp_full);
+            if (j + 1 == n) umma_commit(&bars->fix_empty);
           }
+          ++tiles;
         }
-        if (!ok) return;
-        if (lane == 0) {
-          umma_commit(&bars->dp_full);
-          if (j + 1 == nkt) umma_commit(&bars->fix_empty);
-        }
-        ++tiles;
-      };
-      scores(0);
-      for (int j = 0; j < nkt && ok; ++j) {
-        if (j + 1 < nkt) scores(j + 1);
-        if (!ok) break;
-        ok = uwait(&bars->ds_full, done, 696);
-        if (!ok) break;
-        ++done;
-        if (lane == 0) {
-          tc_fence_after();
-          const uint32_t pk = base + (uint32_t)j * (VC + KC) + VC;
-#pragma unroll
-          for (int c = 0; c < KC; ++c) {
-            const uint64_t k = rd + (uint64_t)((pk + c) % NS * (kPiece >> 4));
+        if (j > 0) {
+          const uint32_t done = tiles - (j < n ? 2 : 1);   // number of tile j - 1
+          ok = uwait(&bars->ds_full, done, 696);
+          if (!ok) break;
+          if (elect_one()) {
+            tc_fence_after();
+            const uint64_t k = kt + (uint64_t)((done & 1) * (kKStage >> 4));
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              umma_ts(tmem + kColDQ + 64 * c, tmem + kColDS + kk * 8, k + (uint64_t)(kk * (2048 >> 4)), id_g,
-                      (j | kk) ? 1u : 0u);
-            umma_commit(&bars->empty[(pk + c) % NS]);
+              umma_ts(tm + kColDQ, tm + kColDS + kk * 8, k + (uint64_t)(kk * (2048 >> 4)), id_k, (j > 1 || kk) ? 1u : 0u);
+            umma_commit(&bars->k_empty[done & 1]);
+            umma_commit(&bars->ds_free);
+            if (j == n) umma_commit(&bars->acc_full);
           }
-          umma_commit(&bars->ds_free);
-          if (j + 1 == nkt) umma_commit(&bars->acc_full);
         }
+        __syncwarp();
       }
-      rg.pos = base + (uint32_t)nkt * (VC + KC);
     }
-    if (lane == 0) {
+    if (elect_one()) {
       umma_commit(&bars->drain);
       mbar_wait_drain(&bars->drain, 0);
     }
