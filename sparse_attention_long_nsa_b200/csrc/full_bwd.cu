@@ -28,7 +28,8 @@ namespace nsa {
 
 namespace {
 
-constexpr int kThreads = 384;   // 8 warps of elementwise work, loads, products, row values, one idle
+constexpr int kThreads = 608;   // 16 warps of elementwise work, loads, products, row values
+constexpr int kEl = 512;        // elementwise threads: four warps share a row's columns, 32 each
 constexpr int kPiece = 16384;   // 128 rows x 64 channels, 128-byte swizzled
 constexpr int kRows = 128;
 
@@ -166,17 +167,17 @@ __device__ __forceinline__ void bwd_init(BwdBars* bars) {
   mbar_init(&bars->fix_full, 1);
   mbar_init(&bars->fix_empty, 1);
   mbar_init(&bars->s_full, 1);
-  mbar_init(&bars->s_read, 256);
-  mbar_init(&bars->p_full, 256);
+  mbar_init(&bars->s_read, kEl);
+  mbar_init(&bars->p_full, kEl);
   mbar_init(&bars->dp_full, 1);
-  mbar_init(&bars->dp_read, 256);
-  mbar_init(&bars->ds_full, 256);
+  mbar_init(&bars->dp_read, kEl);
+  mbar_init(&bars->ds_full, kEl);
   mbar_init(&bars->ds_free, 1);
   mbar_init(&bars->acc_full, 1);
   mbar_init(&bars->drain, 1);
   for (int i = 0; i < 2; ++i) {
     mbar_init(&bars->row_full[i], 32);
-    mbar_init(&bars->row_empty[i], 256);
+    mbar_init(&bars->row_empty[i], kEl);
   }
   bars->abort = 0;
   fence_mbar_init();
@@ -201,8 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
   uint8_t* Vs = Ks + KC * kPiece;
   uint8_t* Qr = Vs + kVStage;               // streamed Q, dO
   uint8_t* Gr = Qr + 2 * kKStage;
-  float2* rowv = reinterpret_cast<float2*>(Gr + VS * kVStage);    // [2][128] (lse, delta) of the row tile
-  BwdBars* bars = reinterpret_cast<BwdBars*>(rowv + 2 * kRows);
+  float* rowv = reinterpret_cast<float*>(Gr + VS * kVStage);      // [2][-lse | -delta][128] of the row tile
+  BwdBars* bars = reinterpret_cast<BwdBars*>(rowv + 4 * kRows);
   volatile int* abort_flag = &bars->abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) bwd_init(bars);
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
     return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, abort_flag, a.status, site));
   };
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ------------------------------------------------------------ loads
     uint32_t k_n = 0, v_n = 0;   // stages filled
     uint32_t tiles = 0;
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
       }
     }
     if (!ok && lane == 0) drain_loads(bars, segs, k_n, v_n, VS);
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ------------------------------------------------------------ products
     // (operands uniform over the warp, see the forward kernel)
     const uint32_t tm = uni(tmem);
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
       mbar_wait_drain(&bars->drain, 0);
     }
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == 18) {
     // ------------------------------------------------------------ (lse, delta) of the row tiles
     uint32_t tiles = 0;
     while (ok && sched.next(sg)) {
@@ -358,92 +359,98 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = i * 32 + lane, t = t0 + r / a.G;
-          rowv[st * kRows + r] = t < sg.L ? a.row[(sg.tok0 + t) * a.H_q + sg.g * a.G + r % a.G] : make_float2(0.f, 0.f);
+          const float2 v = t < sg.L ? a.row[(sg.tok0 + t) * a.H_q + sg.g * a.G + r % a.G] : make_float2(0.f, 0.f);
+          rowv[st * 2 * kRows + r] = -v.x;
+          rowv[(st * 2 + 1) * kRows + r] = -v.y;
         }
         mbar_arrive(&bars->row_full[st]);
       }
     }
-  } else if (warp < 8) {
+  } else if (warp < 16) {
     // ------------------------------------------------------------ P, dS; results
-    const int half = warp >> 2;                      // rows 64 half .. + 63 of the tile
+    const int wq = warp >> 2;                        // rows 32 wq .. + 31 of the tile
     const int r = (warp & 3) * 32 + lane;            // key = tensor-memory lane
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const float sc = a.scale_log2;
+    const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
     uint32_t tiles = 0;
     int segs = 0;
     while (ok && sched.next(sg)) {
       const int key = sg.kt * kRows + r;
+#pragma unroll 1
       for (int j = 0; j < sg.n && ok; ++j, ++tiles) {
         const int t0 = (sg.r0 + j) * TOK;
         const bool edge = t0 < sg.kt * kRows + kRows - 1 || t0 + TOK > sg.L;
-        // rows lo <= c < hi of this half see the key
-        const int lo = max(key - t0, 0) * a.G - 64 * half, hi = min(sg.L - t0, TOK) * a.G - 64 * half;
-        const float2* rv = rowv + (tiles & 1) * kRows + 64 * half;
-        ok = uwait(&bars->row_full[tiles & 1], tiles >> 1, 671) && uwait(&bars->s_full, tiles, 672);
+        // rows lo <= c < hi of these see the key
+        const int lo = max(key - t0, 0) * a.G - 32 * wq, hi = min(sg.L - t0, TOK) * a.G - 32 * wq;
+        const float* rv = rowv + (tiles & 1) * 2 * kRows + 32 * wq;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->row_full[tiles & 1], (tiles >> 1) & 1, abort_flag, a.status, 671) &&
+                                         mbar_wait(&bars->s_full, tiles & 1, abort_flag, a.status, 672));
         if (!ok) break;
         tc_fence_after();
-        float p[64];
-        tmem_ld32(tmem + lane_base + 64 * half, p);
-        tmem_ld32(tmem + lane_base + 64 * half + 32, p + 32);
+        float p[32];
+        tmem_ld32(tmem + lane_base + 32 * wq, p);
         tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 64; ++c) asm volatile("" : "+f"(p[c]));   // no use before the wait
+        for (int c = 0; c < 32; ++c) asm volatile("" : "+f"(p[c]));   // no use before the wait
         tc_fence_before();
         mbar_arrive(&bars->s_read);
+        uint32_t w[16];
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
+        for (int c = 0; c < 32; c += 4) {
           const float4 v = *reinterpret_cast<const float4*>(rv + c);
-          p[c] = ex2(fmaf(p[c], sc, -v.x));
-          p[c + 1] = ex2(fmaf(p[c + 1], sc, -v.z));
+          const float2 e0 = fma2(make_float2(p[c], p[c + 1]), sc2, make_float2(v.x, v.y));
+          const float2 e1 = fma2(make_float2(p[c + 2], p[c + 3]), sc2, make_float2(v.z, v.w));
+          p[c] = ex2(e0.x);
+          p[c + 1] = ex2(e0.y);
+          p[c + 2] = ex2(e1.x);
+          p[c + 3] = ex2(e1.y);
         }
         if (edge) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c) p[c] = (c >= lo && c < hi) ? p[c] : 0.f;
+          for (int c = 0; c < 32; ++c) p[c] = (c >= lo && c < hi) ? p[c] : 0.f;
         }
-        // P^T lies over columns that the other half's warps read
+#pragma unroll
+        for (int c = 0; c < 16; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+        // P^T lies over columns that other warps read
         ok = uwait(&bars->s_read, tiles, 673);
         if (!ok) break;
         tc_fence_after();
-        {
-          uint32_t w[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
-          tmem_st32(tmem + lane_base + 32 * half, w);
-        }
+        tmem_st16(tmem + lane_base + 16 * wq, w);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&bars->p_full);
         ok = uwait(&bars->dp_full, tiles, 674);
         if (!ok) break;
         tc_fence_after();
-        uint32_t w[32];
+        float d[32];
+        tmem_ld32(tmem + lane_base + kColDP + 32 * wq, d);
+        tmem_ld_wait();
 #pragma unroll
-        for (int c0 = 0; c0 < 64; c0 += 32) {
-          float d[32];
-          tmem_ld32(tmem + lane_base + kColDP + 64 * half + c0, d);
-          tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < 32; ++c) asm volatile("" : "+f"(d[c]));
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float4 v = *reinterpret_cast<const float4*>(rv + c0 + c);
-            d[c] = p[c0 + c] * (d[c] - v.y);
-            d[c + 1] = p[c0 + c + 1] * (d[c + 1] - v.w);
-          }
-          if (edge) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) d[c] = (c0 + c >= lo && c0 + c < hi) ? d[c] : 0.f;
-          }
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) w[(c0 + c) >> 1] = pack_bf16x2(d[c], d[c + 1]);
-        }
+        for (int c = 0; c < 32; ++c) asm volatile("" : "+f"(d[c]));
         tc_fence_before();
-        mbar_arrive(&bars->row_empty[tiles & 1]);
         mbar_arrive(&bars->dp_read);
-        ok = uwait(&bars->dp_read, tiles, 675);   // dS^T lies over columns that the other half's warps read
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(rv + kRows + c);
+          const float2 d0 = mul2(make_float2(p[c], p[c + 1]), add2(make_float2(d[c], d[c + 1]), make_float2(v.x, v.y)));
+          const float2 d1 =
+              mul2(make_float2(p[c + 2], p[c + 3]), add2(make_float2(d[c + 2], d[c + 3]), make_float2(v.z, v.w)));
+          d[c] = d0.x;
+          d[c + 1] = d0.y;
+          d[c + 2] = d1.x;
+          d[c + 3] = d1.y;
+        }
+        mbar_arrive(&bars->row_empty[tiles & 1]);
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) d[c] = (c >= lo && c < hi) ? d[c] : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < 16; ++c) w[c] = pack_bf16x2(d[2 * c], d[2 * c + 1]);
+        ok = uwait(&bars->dp_read, tiles, 675);   // dS^T lies over columns that other warps read
         if (!ok) break;
         tc_fence_after();
-        tmem_st32(tmem + lane_base + kColDP + 32 * half, w);
+        tmem_st16(tmem + lane_base + kColDP + 16 * wq, w);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&bars->ds_full);
@@ -452,18 +459,15 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
       ok = uwait(&bars->acc_full, segs++, 676);
       if (!ok) break;
       tc_fence_after();
-      // warps 0-3 write dV, warps 4-7 dK
-      const int D = half == 0 ? DV : DK;
-      const uint32_t col = half == 0 ? kColDV : kColDK;
-      const float f = half == 0 ? 1.f : a.scale;
+      // 32 columns at a time of dV and dK, dealt to the warps that share the rows
       const bool valid = key < sg.L;
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(half == 0 ? a.dv : a.dk) +
-                           ((sg.tok0 + key) * a.H_kv + sg.g) * D;
-      float* part = a.part + ((int64_t)sg.slot * kRows + r) * (DK + DV) + (half == 0 ? 0 : DV);
+      const int64_t row = (sg.tok0 + key) * a.H_kv + sg.g;
+      float* part = a.part + ((int64_t)sg.slot * kRows + r) * (DK + DV);
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = 32 * wq; c < DV + DK; c += 128) {
+        const bool is_v = c < DV;
         float d[32];
-        tmem_ld32(tmem + lane_base + col + c, d);
+        tmem_ld32(tmem + lane_base + (is_v ? kColDV + c : kColDK + c - DV), d);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(d[i]));
@@ -473,12 +477,16 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
             for (int i = 0; i < 32; i += 4)
               *reinterpret_cast<float4*>(part + c + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
           } else {
+            __nv_bfloat16* dst = is_v ? static_cast<__nv_bfloat16*>(a.dv) + row * DV + c
+                                      : static_cast<__nv_bfloat16*>(a.dk) + row * DK + c - DV;
+            const float f = is_v ? 1.f : a.scale;
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4*>(dst + c + i) = pack_out(d + i, f);
+            for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4*>(dst + i) = pack_out(d + i, f);
           }
         }
         __syncwarp();   // the tensor-memory loads are warp-wide
       }
+      tc_fence_before();   // the next unit's products wait for this thread's next arrivals
     }
   }
   tc_fence_before();
@@ -580,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_q_kernel(const FullB
     return true;
   };
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ------------------------------------------------------------ loads
     uint32_t k_n = 0, v_n = 0;   // stages filled
     uint32_t tiles = 0;
@@ -617,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_q_kernel(const FullB
       }
     }
     if (!ok && lane == 0) drain_loads(bars, segs, k_n, v_n, VS);
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ------------------------------------------------------------ products
     // S and dP of tile j + 1 are issued before dQ of tile j: both stages of K are in
     // use then, V(j) is released by its dP
@@ -700,12 +708,12 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_q_kernel(const FullB
       mbar_wait_drain(&bars->drain, 0);
     }
     __syncwarp();
-  } else if (warp < 8) {
+  } else if (warp < 16) {
     // ------------------------------------------------------------ dS; dQ
-    const int half = warp >> 2;                      // keys 64 half .. + 63 of the tile
+    const int wq = warp >> 2;                        // keys 32 wq .. + 31 of the tile
     const int r = (warp & 3) * 32 + lane;            // row = tensor-memory lane
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const float sc = a.scale_log2;
+    const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
     uint32_t tiles = 0;
     int segs = 0;
     while (ok && next()) {
@@ -713,51 +721,56 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_q_kernel(const FullB
       const bool valid = t < L;
       const int64_t row = (tok0 + t) * a.H_q + hq;
       const float2 rv = valid ? a.row[row] : make_float2(0.f, 0.f);
+      const float2 nl = make_float2(-rv.x, -rv.x), nd = make_float2(-rv.y, -rv.y);
+#pragma unroll 1
       for (int j = 0; j < nkt && ok; ++j, ++tiles) {
-        const int k0 = j * kRows + 64 * half;
         const bool edge = j * kRows + kRows - 1 > i0;   // some key of the tile is past the first token
-        const int hi = t - k0;                          // keys c <= hi are seen
+        const int hi = t - (j * kRows + 32 * wq);       // keys c <= hi are seen
         ok = uwait(&bars->s_full, tiles, 701);
         if (!ok) break;
         tc_fence_after();
-        float p[64];
-        tmem_ld32(tmem + lane_base + 64 * half, p);
-        tmem_ld32(tmem + lane_base + 64 * half + 32, p + 32);
+        float p[32];
+        tmem_ld32(tmem + lane_base + 32 * wq, p);
         tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 64; ++c) asm volatile("" : "+f"(p[c]));
+        for (int c = 0; c < 32; ++c) asm volatile("" : "+f"(p[c]));
         tc_fence_before();
         mbar_arrive(&bars->s_read);
 #pragma unroll
-        for (int c = 0; c < 64; ++c) p[c] = ex2(fmaf(p[c], sc, -rv.x));
+        for (int c = 0; c < 32; c += 2) {
+          const float2 e = fma2(make_float2(p[c], p[c + 1]), sc2, nl);
+          p[c] = ex2(e.x);
+          p[c + 1] = ex2(e.y);
+        }
         ok = uwait(&bars->dp_full, tiles, 702);
         if (!ok) break;
         tc_fence_after();
-        uint32_t w[32];
+        float d[32];
+        tmem_ld32(tmem + lane_base + kColDP + 32 * wq, d);
+        tmem_ld_wait();
 #pragma unroll
-        for (int c0 = 0; c0 < 64; c0 += 32) {
-          float d[32];
-          tmem_ld32(tmem + lane_base + kColDP + 64 * half + c0, d);
-          tmem_ld_wait();
-#pragma unroll
-          for (int c = 0; c < 32; ++c) asm volatile("" : "+f"(d[c]));
-#pragma unroll
-          for (int c = 0; c < 32; ++c) d[c] = p[c0 + c] * (d[c] - rv.y);
-          if (edge) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) d[c] = c0 + c <= hi ? d[c] : 0.f;
-          }
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) w[(c0 + c) >> 1] = pack_bf16x2(d[c], d[c + 1]);
-        }
+        for (int c = 0; c < 32; ++c) asm volatile("" : "+f"(d[c]));
         tc_fence_before();
         mbar_arrive(&bars->dp_read);
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const float2 v = mul2(make_float2(p[c], p[c + 1]), add2(make_float2(d[c], d[c + 1]), nd));
+          d[c] = v.x;
+          d[c + 1] = v.y;
+        }
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) d[c] = c <= hi ? d[c] : 0.f;
+        }
+        uint32_t w[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) w[c] = pack_bf16x2(d[2 * c], d[2 * c + 1]);
         if (tiles > 0) {   // the product that reads the tile before has finished
           ok = uwait(&bars->ds_free, tiles - 1, 703);
           if (!ok) break;
           tc_fence_after();
         }
-        tmem_st32(tmem + lane_base + kColDS + 32 * half, w);
+        tmem_st16(tmem + lane_base + kColDS + 16 * wq, w);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&bars->ds_full);
@@ -766,11 +779,11 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_q_kernel(const FullB
       ok = uwait(&bars->acc_full, segs++, 704);
       if (!ok) break;
       tc_fence_after();
-      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dq) + row * DK + half * (DK / 2);
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dq) + row * DK;
 #pragma unroll 1
-      for (int c = 0; c < DK / 2; c += 32) {
+      for (int c = 32 * wq; c < DK; c += 128) {
         float d[32];
-        tmem_ld32(tmem + lane_base + kColDQ + half * (DK / 2) + c, d);
+        tmem_ld32(tmem + lane_base + kColDQ + c, d);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(d[i]));
@@ -780,6 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_q_kernel(const FullB
         }
         __syncwarp();
       }
+      tc_fence_before();
     }
   }
   tc_fence_before();
