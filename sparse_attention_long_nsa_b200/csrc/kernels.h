@@ -216,7 +216,7 @@ struct RopeArgs {
   int H_q, H_kv, H_v;     // H_v: value heads to copy (0 or H_kv)
   int d_v, d_rot, interleaved;
   float eps;
-  int tok;                // tokens per block
+  int wpt;                // warps that share a token
   void *q_out, *k_out, *v_out;
 };
 constexpr int kRopeBwdBlocks = 296;   // two per SM

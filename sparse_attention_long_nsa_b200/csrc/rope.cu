@@ -17,9 +17,10 @@
 // a head: a lane holds d_k / 64 units, a unit being two 8-byte chunks of 4 channels
 // (with 16-byte chunks and four lanes the backward's sums of dw alone took 48
 // registers and it spilled). For pairs (i, i + d_rot / 2) the two chunks of a
-// rotating unit are partners, so that every rotation stays inside a thread. The
-// sines and cosines of a block's tokens are computed once into shared memory and
-// serve all heads; a head's channels are loaded while the head before is worked on.
+// rotating unit are partners, so that every rotation stays inside a thread. A warp
+// takes one token and four heads at a time: it forms the token's sines and cosines
+// (and, forward, their products with the weights) once, in registers, for all of its
+// heads; formed per head their loads and the index arithmetic bound the kernel.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -29,7 +30,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kLanes = 8;                       // of a head
-constexpr int kGroups = kThreads / kLanes;      // heads in work at a time
+constexpr int kWarps = kThreads / 32;
+constexpr int kWarpHeads = 32 / kLanes;         // heads a warp works on at a time
 
 struct Chunks {
   int c0, c1;   // the two 4-channel chunks of a unit
@@ -60,45 +62,50 @@ __device__ __forceinline__ float sum8(float x) {
   return x;
 }
 
-// cosine and sine of pair i of tokens n0 .. n0 + nt - 1 into cosv / sinv[tok * half + i]
-__device__ __forceinline__ void fill_angles(const RopeArgs& a, int64_t n0, int nt, int half, float* cosv, float* sinv) {
+// cosine and sine of a token's pairs into cosv / sinv (one warp)
+__device__ __forceinline__ void fill_angles(const RopeArgs& a, int64_t n, int half, float* cosv, float* sinv) {
   constexpr double k2Pi = 6.283185307179586476925286766559, kInv2Pi = 0.15915494309189533576888376337251;
-  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-    const int tok = i / half;
-    const double x = (double)a.positions[n0 + tok] * (double)a.inv_freq[i - tok * half];
+  const double pos = (double)a.positions[n];
+  __syncwarp();   // the token before is done with them
+  for (int i = threadIdx.x & 31; i < half; i += 32) {
+    const double x = pos * (double)a.inv_freq[i];
     const float r = (float)fma(-rint(x * kInv2Pi), k2Pi, x);
     float s, c;
     sincosf(r, &s, &c);
     cosv[i] = c;
     sinv[i] = s;
   }
+  __syncwarp();
 }
 
-// turn the pairs of a unit (SIGN -1: by the opposite angle); f[0..3] and f[4..7]
-// are its two chunks, first channel 4 * c0 / 4 * c1; cv, sv: the token's row
-template <bool INTER, int SIGN>
-__device__ __forceinline__ void turn_unit(float* f, const Chunks& ch, const float* cv, const float* sv) {
+// the cosines and sines of a unit's four pairs ((1, 0) when it does not rotate):
+// pair i is channels (i, 4 + i), interleaved (2i, 2i + 1)
+template <bool INTER>
+__device__ __forceinline__ void unit_angles(const Chunks& ch, const float* cv, const float* sv, float* c, float* s) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = INTER ? (i < 2 ? ch.c0 * 2 + i : ch.c1 * 2 + i - 2) : ch.c0 * 4 + i;
+    c[i] = ch.rot ? cv[at] : 1.f;
+    s[i] = ch.rot ? sv[at] : 0.f;
+  }
+}
+
+// out pair i = (a A_i + b B_i, a C_i + b D_i) of a unit's pairs (a, b), co = A, B, C, D
+template <bool INTER>
+__device__ __forceinline__ void mix_unit(float* f, const float (*co)[4]) {
   if constexpr (INTER) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int at = (h == 0 ? ch.c0 : ch.c1) * 2;
-      const float2 c2 = *reinterpret_cast<const float2*>(cv + at), s2 = *reinterpret_cast<const float2*>(sv + at);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float c = i == 0 ? c2.x : c2.y, s = SIGN * (i == 0 ? s2.x : s2.y);
-        const float p = f[4 * h + 2 * i], q = f[4 * h + 2 * i + 1];
-        f[4 * h + 2 * i] = fmaf(q, -s, p * c);
-        f[4 * h + 2 * i + 1] = fmaf(p, s, q * c);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const float p = f[2 * i], q = f[2 * i + 1];
+      f[2 * i] = fmaf(q, co[1][i], p * co[0][i]);
+      f[2 * i + 1] = fmaf(p, co[2][i], q * co[3][i]);
     }
   } else {
-    const float4 c4 = *reinterpret_cast<const float4*>(cv + ch.c0 * 4), s4 = *reinterpret_cast<const float4*>(sv + ch.c0 * 4);
 #pragma unroll
     for (int k = 0; k < 4; k += 2) {
-      const float2 c = k == 0 ? make_float2(c4.x, c4.y) : make_float2(c4.z, c4.w);
-      const float2 s = k == 0 ? make_float2(SIGN * s4.x, SIGN * s4.y) : make_float2(SIGN * s4.z, SIGN * s4.w);
       const float2 p = make_float2(f[k], f[k + 1]), q = make_float2(f[4 + k], f[5 + k]);
-      const float2 y = fma2(q, make_float2(-s.x, -s.y), mul2(p, c)), z = fma2(p, s, mul2(q, c));
+      const float2 y = fma2(q, make_float2(co[1][k], co[1][k + 1]), mul2(p, make_float2(co[0][k], co[0][k + 1])));
+      const float2 z = fma2(p, make_float2(co[2][k], co[2][k + 1]), mul2(q, make_float2(co[3][k], co[3][k + 1])));
       f[k] = y.x;
       f[k + 1] = y.y;
       f[4 + k] = z.x;
@@ -139,140 +146,143 @@ __device__ __forceinline__ void load_head(const __nv_bfloat16* x, bool on, int s
 
 }  // namespace
 
-// One block: `tok` tokens, all their query, key (and value) heads, dealt to the 32
-// lane groups in turn. Values are copied.
+// `wpt` warps share a token's heads; a block has 8 / wpt tokens. Values are copied.
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) nsa_qk_norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) nsa_qk_norm_rope_kernel(const RopeArgs a) {
   constexpr int U = D / 64;
-  extern __shared__ float4 sm_angles[];   // cosines, then sines
-  float* cosv = reinterpret_cast<float*>(sm_angles);
-  const int64_t n0 = (int64_t)blockIdx.x * a.tok;
-  const int nt = (int)min((int64_t)a.tok, a.N - n0);
+  extern __shared__ float4 sm_angles[];   // cosines and sines of each warp's token
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane & (kLanes - 1), grp = lane / kLanes;
+  const int64_t n = (int64_t)blockIdx.x * (kWarps / a.wpt) + warp / a.wpt;
+  if (n >= a.N) return;   // the whole warp; the warps of a block do not meet
+  const int first = (warp % a.wpt) * kWarpHeads + grp, step = a.wpt * kWarpHeads;
   const int half = a.d_rot >> 1, R = a.d_rot >> 2;
-  float* sinv = cosv + a.tok * half;
-  const int sub = threadIdx.x & (kLanes - 1), grp = threadIdx.x / kLanes;
-  const int H = a.H_q + a.H_kv, HA = H + a.H_v;
-  const int total = nt * HA;
-  struct Item {
-    int64_t n;
-    int tok, h;
-    bool on;
-  };
-  auto item_of = [&](int i) -> Item {
-    Item it;
-    it.on = i < total;
-    it.tok = it.on ? i / HA : 0;
-    it.h = it.on ? i - it.tok * HA : 0;
-    it.n = n0 + it.tok;
-    return it;
-  };
-  auto src = [&](const Item& it) -> const __nv_bfloat16* {
-    return it.h < a.H_q ? static_cast<const __nv_bfloat16*>(a.q) + it.n * a.q_stride + (int64_t)it.h * D
-                        : static_cast<const __nv_bfloat16*>(a.k) + it.n * a.k_stride + (int64_t)(it.h - a.H_q) * D;
-  };
-  Item it = item_of(grp);
-  uint2 raw[U][2], nxt[U][2];
-  load_head<U>(src(it), it.on && it.h < H, sub, R, raw);
-  fill_angles(a, n0, nt, half, cosv, sinv);
-  __syncthreads();
-  for (int base = 0; base < total; base += kGroups) {
-    const Item ni = item_of(base + kGroups + grp);
-    load_head<U>(src(ni), ni.on && ni.h < H, sub, R, nxt);
-    const bool is_q = it.h < a.H_q, is_v = it.h >= H;
-    int64_t row = it.n;
-    bool write = it.on;
-    if (!is_q && a.cache_rows) {   // a row outside the cache is not written
-      row = a.cache_rows[it.n];
-      write = it.on && row >= 0 && row < a.n_rows;
-    }
-    if (is_v && write) {
-      const int hv = it.h - H;
-      const uint4* s4 = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + it.n * a.v_stride +
-                                                       (int64_t)hv * a.d_v);
-      uint4* d4 = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.v_out) + (row * a.H_kv + hv) * a.d_v);
-      for (int c = sub; c < a.d_v / 8; c += kLanes) d4[c] = s4[c];
-    }
-    float2 s2 = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < U; ++j) s2 = square_sum(raw[j], s2);
-    const float r = rsqrtf(sum8(s2.x + s2.y) * (1.f / D) + a.eps);
-    if (write && !is_v) {
-      const float* w = is_q ? a.w_q : a.w_k;
-      __nv_bfloat16* y = is_q ? static_cast<__nv_bfloat16*>(a.q_out) + (it.n * a.H_q + it.h) * D
-                              : static_cast<__nv_bfloat16*>(a.k_out) + (row * a.H_kv + it.h - a.H_q) * D;
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const Chunks ch = unit_chunks(sub + kLanes * j, R);
-        float f[8], wv[8];
-        unpack4(raw[j][0], f);
-        unpack4(raw[j][1], f + 4);
-        load_w(w, ch, wv);
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const float2 v = mul2(make_float2(f[i], f[i + 1]), mul2(make_float2(wv[i], wv[i + 1]), make_float2(r, r)));
-          f[i] = v.x;
-          f[i + 1] = v.y;
-        }
-        if (ch.rot) turn_unit<INTER, 1>(f, ch, cosv + it.tok * half, sinv + it.tok * half);
-        reinterpret_cast<uint2*>(y)[ch.c0] = pack4(f);
-        reinterpret_cast<uint2*>(y)[ch.c1] = pack4(f + 4);
-      }
-    }
-    it = ni;
+  float* cosv = reinterpret_cast<float*>(sm_angles) + warp * a.d_rot;
+  float* sinv = cosv + half;
+  int64_t row = n;   // of the key and value; a row outside the cache is not written
+  if (a.cache_rows) row = a.cache_rows[n];
+  const bool store_kv = row >= 0 && (!a.cache_rows || row < a.n_rows);
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + n * a.q_stride;
+  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.k) + n * a.k_stride;
+  uint2 raw[U][2];
+  load_head<U>(q + (int64_t)first * D, first < a.H_q, sub, R, raw);
+  fill_angles(a, n, half, cosv, sinv);
+#pragma unroll 1
+  for (int role = 0; role < (store_kv ? 2 : 1); ++role) {   // queries, keys
+    const int H = role == 0 ? a.H_q : a.H_kv;
+    const float* w = role == 0 ? a.w_q : a.w_k;
+    const __nv_bfloat16* x = role == 0 ? q : k;
+    __nv_bfloat16* y = role == 0 ? static_cast<__nv_bfloat16*>(a.q_out) + n * a.H_q * D
+                                 : static_cast<__nv_bfloat16*>(a.k_out) + row * a.H_kv * D;
+    if (role == 1) load_head<U>(x + (int64_t)first * D, first < H, sub, R, raw);
+    if (first - grp >= H) continue;   // none for this warp
+    // norm weight and rotation of a pair (a, b) in one: (a w_a c - b w_b s, a w_a s + b w_b c)
+    float co[U][4][4];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      raw[j][0] = nxt[j][0];
-      raw[j][1] = nxt[j][1];
+      const Chunks ch = unit_chunks(sub + kLanes * j, R);
+      float wv[8], c[4], s[4];
+      load_w(w, ch, wv);
+      unit_angles<INTER>(ch, cosv, sinv, c, s);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float wa = INTER ? wv[2 * i] : wv[i], wb = INTER ? wv[2 * i + 1] : wv[4 + i];
+        co[j][0][i] = wa * c[i];
+        co[j][1][i] = -wb * s[i];
+        co[j][2][i] = wa * s[i];
+        co[j][3][i] = wb * c[i];
+      }
+    }
+#pragma unroll 1
+    for (int h = first; h - grp < H; h += step) {
+      uint2 cur[U][2];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        cur[j][0] = raw[j][0];
+        cur[j][1] = raw[j][1];
+      }
+      load_head<U>(x + (int64_t)(h + step) * D, h + step < H, sub, R, raw);
+      float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < U; ++j) s2 = square_sum(cur[j], s2);
+      const float r = rsqrtf(sum8(s2.x + s2.y) * (1.f / D) + a.eps);
+      const float2 r2 = make_float2(r, r);
+      if (h < H) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          const Chunks ch = unit_chunks(sub + kLanes * j, R);
+          float f[8];
+          unpack4(cur[j][0], f);
+          unpack4(cur[j][1], f + 4);
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const float2 v = mul2(make_float2(f[i], f[i + 1]), r2);
+            f[i] = v.x;
+            f[i + 1] = v.y;
+          }
+          mix_unit<INTER>(f, co[j]);
+          uint2* dst = reinterpret_cast<uint2*>(y + (int64_t)h * D);
+          dst[ch.c0] = pack4(f);
+          dst[ch.c1] = pack4(f + 4);
+        }
+      }
+      __syncwarp();
     }
   }
+  if (a.H_v > 0 && store_kv)
+    for (int h = first; h < a.H_v; h += step) {
+      const uint4* s4 = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + n * a.v_stride +
+                                                       (int64_t)h * a.d_v);
+      uint4* d4 = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.v_out) + (row * a.H_kv + h) * a.d_v);
+      for (int c = sub; c < a.d_v / 8; c += kLanes) d4[c] = s4[c];
+    }
 }
 
-// Backward. grid.x blocks walk the token groups; blocks below `q_blocks` take the
-// query heads, the others the key heads, so that a thread's dw sums belong to one
-// weight. part[block][D]: this block's dw, its groups summed in a fixed order.
+// Backward. The blocks below `q_blocks` take the query heads, the others the key
+// heads, so that a thread's dw sums belong to one weight. part[block][D]: this
+// block's dw, its lane groups summed in a fixed order.
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kThreads, 2) nsa_qk_norm_rope_bwd_kernel(const RopeBwdArgs b) {
   constexpr int U = D / 64;
-  extern __shared__ float4 sm_angles[];   // cosines, then sines; at the end the warps' dw
-  float* cosv = reinterpret_cast<float*>(sm_angles);
+  extern __shared__ float4 sm_angles[];   // cosines and sines of each warp's token; at the end the warps' dw
+  __shared__ float4 w_s[D / 4];
   const RopeArgs& a = b.f;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane & (kLanes - 1), grp = lane / kLanes;
   const int half = a.d_rot >> 1, R = a.d_rot >> 2;
-  float* sinv = cosv + a.tok * half;
-  const int sub = threadIdx.x & (kLanes - 1), grp = threadIdx.x / kLanes;
+  float* cosv = reinterpret_cast<float*>(sm_angles) + warp * a.d_rot;
+  float* sinv = cosv + half;
   const bool is_q = (int)blockIdx.x < b.q_blocks;
   const int blk = is_q ? blockIdx.x : blockIdx.x - b.q_blocks;
   const int nblk = is_q ? b.q_blocks : (int)gridDim.x - b.q_blocks;
   const int H = is_q ? a.H_q : a.H_kv;
-  const float* w = is_q ? a.w_q : a.w_k;
+  const float* w = reinterpret_cast<const float*>(w_s);
+  for (int i = threadIdx.x; i < D; i += kThreads) reinterpret_cast<float*>(w_s)[i] = (is_q ? a.w_q : a.w_k)[i];
+  __syncthreads();
   const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(is_q ? a.q : a.k);
   const __nv_bfloat16* gb = static_cast<const __nv_bfloat16*>(is_q ? b.dq_out : b.dk_out);
   __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(is_q ? b.dq : b.dk);
   const int64_t xs = is_q ? a.q_stride : a.k_stride, os = is_q ? b.dq_stride : b.dk_stride;
+  const int first = (warp % a.wpt) * kWarpHeads + grp, step = a.wpt * kWarpHeads;
   float dw[U][8];
 #pragma unroll
   for (int j = 0; j < U; ++j)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
-  for (int64_t n0 = (int64_t)blk * a.tok; n0 < a.N; n0 += (int64_t)nblk * a.tok) {
-    const int nt = (int)min((int64_t)a.tok, a.N - n0);
-    const int total = nt * H;
+  const int per = kWarps / a.wpt;   // tokens of a block at a time
+#pragma unroll 1
+  for (int64_t n = (int64_t)blk * per + warp / a.wpt; n < a.N; n += (int64_t)nblk * per) {
     uint2 rx[U][2], rg[U][2];
-    auto load = [&](int i) {
-      const bool on = i < total;
-      const int tok = on ? i / H : 0, h = on ? i - tok * H : 0;
-      load_head<U>(xb + (n0 + tok) * xs + (int64_t)h * D, on, sub, R, rx);
-      load_head<U>(gb + ((n0 + tok) * H + h) * D, on, sub, R, rg);
-    };
-    load(grp);
-    __syncthreads();
-    fill_angles(a, n0, nt, half, cosv, sinv);
-    __syncthreads();
-    for (int base = 0; base < total; base += kGroups) {
-      const int item = base + grp;
-      const bool on = item < total;
-      const int tok = on ? item / H : 0;
-      const int h = on ? item - tok * H : 0;
-      const int64_t n = n0 + tok;
+    const __nv_bfloat16* x = xb + n * xs;
+    const __nv_bfloat16* g = gb + n * H * D;
+    load_head<U>(x + (int64_t)first * D, first < H, sub, R, rx);
+    load_head<U>(g + (int64_t)first * D, first < H, sub, R, rg);
+    fill_angles(a, n, half, cosv, sinv);
+    float c[U][4], s[U][4];   // the token's angles of this lane's units
+#pragma unroll
+    for (int j = 0; j < U; ++j) unit_angles<INTER>(unit_chunks(sub + kLanes * j, R), cosv, sinv, c[j], s[j]);
+#pragma unroll 1
+    for (int h = first; h - grp < H; h += step) {
       uint2 cx[U][2], cg[U][2];
 #pragma unroll
       for (int j = 0; j < U; ++j)
@@ -281,13 +291,14 @@ __global__ void __launch_bounds__(kThreads, 2) nsa_qk_norm_rope_bwd_kernel(const
           cx[j][i] = rx[j][i];
           cg[j][i] = rg[j][i];
         }
-      if (base + kGroups < total) load(item + kGroups);
+      load_head<U>(x + (int64_t)(h + step) * D, h + step < H, sub, R, rx);
+      load_head<U>(g + (int64_t)(h + step) * D, h + step < H, sub, R, rg);
       float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
       for (int j = 0; j < U; ++j) s2 = square_sum(cx[j], s2);
       const float r = rsqrtf(sum8(s2.x + s2.y) * (1.f / D) + a.eps);
       const float2 r2 = make_float2(r, r);
-      // u = dn w (dn: the gradient turned back); dw += dn h; m = sum(u h), h = x r
+      // dn: the gradient turned back; u = dn w; dw += dn h; m = sum(u h), h = x r
       float u[U][8];
       float2 m2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -298,7 +309,11 @@ __global__ void __launch_bounds__(kThreads, 2) nsa_qk_norm_rope_bwd_kernel(const
         unpack4(cg[j][1], u[j] + 4);
         unpack4(cx[j][0], f);
         unpack4(cx[j][1], f + 4);
-        if (ch.rot) turn_unit<INTER, -1>(u[j], ch, cosv + tok * half, sinv + tok * half);
+        const float co[4][4] = {{c[j][0], c[j][1], c[j][2], c[j][3]},
+                                {s[j][0], s[j][1], s[j][2], s[j][3]},
+                                {-s[j][0], -s[j][1], -s[j][2], -s[j][3]},
+                                {c[j][0], c[j][1], c[j][2], c[j][3]}};
+        mix_unit<INTER>(u[j], co);
         load_w(w, ch, wv);
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
@@ -313,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 2) nsa_qk_norm_rope_bwd_kernel(const
         }
       }
       const float m = -sum8(m2.x + m2.y) * (1.f / D) * r;   // -mean(u h) r: h = x r below
-      if (on) {
+      if (h < H) {
         uint2* dst = reinterpret_cast<uint2*>(ob + n * os + (int64_t)h * D);
 #pragma unroll
         for (int j = 0; j < U; ++j) {
@@ -331,29 +346,29 @@ __global__ void __launch_bounds__(kThreads, 2) nsa_qk_norm_rope_bwd_kernel(const
           dst[ch.c1] = pack4(f + 4);
         }
       }
+      __syncwarp();
     }
   }
   // this block's dw: over the 4 lane groups of a warp by shuffles, then over the warps
   __syncthreads();
-  float* red = cosv;   // [8 warps][D]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* red = reinterpret_cast<float*>(sm_angles);   // [8 warps][D]
 #pragma unroll
   for (int j = 0; j < U; ++j) {
     const Chunks ch = unit_chunks(sub + kLanes * j, R);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float s = dw[j][i];
-      s += __shfl_xor_sync(0xffffffffu, s, 8);
-      s += __shfl_xor_sync(0xffffffffu, s, 16);
-      if (lane < kLanes) red[warp * D + (i < 4 ? ch.c0 * 4 + i : ch.c1 * 4 + i - 4)] = s;
+      float t = dw[j][i];
+      t += __shfl_xor_sync(0xffffffffu, t, 8);
+      t += __shfl_xor_sync(0xffffffffu, t, 16);
+      if (lane < kLanes) red[warp * D + (i < 4 ? ch.c0 * 4 + i : ch.c1 * 4 + i - 4)] = t;
     }
   }
   __syncthreads();
   for (int e = threadIdx.x; e < D; e += kThreads) {
-    float s = 0.f;
+    float t = 0.f;
 #pragma unroll
-    for (int v = 0; v < kThreads / 32; ++v) s += red[v * D + e];
-    b.part[(size_t)blockIdx.x * D + e] = s;
+    for (int v = 0; v < kWarps; ++v) t += red[v * D + e];
+    b.part[(size_t)blockIdx.x * D + e] = t;
   }
 }
 
@@ -375,17 +390,19 @@ __global__ void __launch_bounds__(256) nsa_rope_dw_kernel(const float* part, int
   }
 }
 
-// tokens per block: enough blocks for two per SM when there are few tokens, at
-// most 8 tokens (the angles of a block serve its tokens' heads only)
-static int rope_tok(int64_t N) {
-  const int64_t t = N / (2 * 148);
-  return t < 1 ? 1 : (t > 8 ? 8 : (int)t);
+// Warps that share a token: as many as its heads can use while the tokens alone do
+// not give every SM two blocks (a decode step of 32 tokens: 8; from 2368 tokens on 1).
+static int rope_wpt(int64_t N, int H) {
+  int wpt = 1;
+  while (wpt < kWarps && wpt * kWarpHeads < H && N * wpt < 2 * 148 * kWarps) wpt *= 2;
+  return wpt;
 }
 
 cudaError_t launch_qk_norm_rope(RopeArgs a, int d_k, cudaStream_t st) {
-  a.tok = rope_tok(a.N);
-  const unsigned grid = (unsigned)((a.N + a.tok - 1) / a.tok);
-  const size_t smem = (size_t)a.tok * a.d_rot * sizeof(float);
+  a.wpt = rope_wpt(a.N, a.H_q);
+  const int per = kWarps / a.wpt;
+  const unsigned grid = (unsigned)((a.N + per - 1) / per);
+  const size_t smem = (size_t)kWarps * a.d_rot * sizeof(float);
 #define NSA_ROPE(D)                                                                            \
   case D:                                                                                      \
     if (a.interleaved) nsa_qk_norm_rope_kernel<D, true><<<grid, kThreads, smem, st>>>(a);      \
@@ -403,16 +420,17 @@ cudaError_t launch_qk_norm_rope(RopeArgs a, int d_k, cudaStream_t st) {
 
 cudaError_t launch_qk_norm_rope_bwd(RopeBwdArgs b, int d_k, cudaStream_t st) {
   RopeArgs& a = b.f;
-  a.tok = rope_tok(a.N);
+  a.wpt = rope_wpt(a.N, a.H_q);
   // two blocks per SM, dealt to queries and keys by their heads
-  const int64_t groups = (a.N + a.tok - 1) / a.tok;
+  const int per = kWarps / a.wpt;
+  const int64_t groups = (a.N + per - 1) / per;
   int kb = (int)((int64_t)kRopeBwdBlocks * a.H_kv / (a.H_q + a.H_kv));
   if (kb < 1) kb = 1;
   int qb = kRopeBwdBlocks - kb;
   if (qb > groups) qb = (int)groups;
   if (kb > groups) kb = (int)groups;
   b.q_blocks = qb;
-  const size_t ang = (size_t)a.tok * a.d_rot * sizeof(float), red = (size_t)(kThreads / 32) * d_k * 4;
+  const size_t ang = (size_t)kWarps * a.d_rot * sizeof(float), red = (size_t)kWarps * d_k * 4;
   const size_t smem = ang > red ? ang : red;
 #define NSA_ROPE(D)                                                                                   \
   case D:                                                                                             \
