@@ -226,8 +226,7 @@ struct RopeBwdArgs {
   void *dq, *dk;          // bf16 gradients of the projections, rows of dq_stride / dk_stride
   int64_t dq_stride, dk_stride;
   float *dw_q, *dw_k;     // fp32 [d_k]
-  float* part;            // fp32 [kRopeBwdBlocks][d_k]
-  int q_blocks;           // blocks that take the query heads
+  float* part;            // fp32 [kRopeBwdBlocks][2][d_k]: a block's dw_q, dw_k
 };
 cudaError_t launch_qk_norm_rope(RopeArgs a, int d_k, cudaStream_t st);
 cudaError_t launch_qk_norm_rope_bwd(RopeBwdArgs b, int d_k, cudaStream_t st);

@@ -1226,7 +1226,7 @@ size_t nsa_full_workspace_size(int op, const nsa_heads_t* heads, int32_t batch, 
     case NSA_OP_TREE_DECODE:
       if (max_len <= 0 || max_nodes <= 0 || max_nodes > NSA_MAX_NODES) return 0;
       return tree_ws(heads, max_nodes).total;
-    case NSA_OP_ROPE_BACKWARD: return 256 + align256((size_t)kRopeBwdBlocks * heads->d_k * 4);
+    case NSA_OP_ROPE_BACKWARD: return 256 + align256((size_t)kRopeBwdBlocks * 2 * heads->d_k * 4);
   }
   return 0;
 }
@@ -1283,7 +1283,7 @@ nsa_status_t nsa_qk_norm_rope_backward(const void* q, int64_t q_stride, const vo
   if (!aligned16(w_q) || !aligned16(w_k) || !aligned16(dq_out) || !aligned16(dk_out) || !aligned16(workspace))
     return NSA_ERR_INVALID_ARG;
   if (N > INT32_MAX) return NSA_ERR_UNSUPPORTED;
-  if (ws_bytes < 256 + align256((size_t)kRopeBwdBlocks * heads->d_k * 4)) return NSA_ERR_WORKSPACE;
+  if (ws_bytes < 256 + align256((size_t)kRopeBwdBlocks * 2 * heads->d_k * 4)) return NSA_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (N == 0) {   // the sums over no tokens
     cudaError_t e = cudaMemsetAsync(dw_q, 0, (size_t)heads->d_k * 4, st);

@@ -82,11 +82,22 @@ __device__ __forceinline__ void fill_angles(const RopeArgs& a, int64_t n, int ha
 // pair i is channels (i, 4 + i), interleaved (2i, 2i + 1)
 template <bool INTER>
 __device__ __forceinline__ void unit_angles(const Chunks& ch, const float* cv, const float* sv, float* c, float* s) {
+  if (!ch.rot) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int at = INTER ? (i < 2 ? ch.c0 * 2 + i : ch.c1 * 2 + i - 2) : ch.c0 * 4 + i;
-    c[i] = ch.rot ? cv[at] : 1.f;
-    s[i] = ch.rot ? sv[at] : 0.f;
+    for (int i = 0; i < 4; ++i) {
+      c[i] = 1.f;
+      s[i] = 0.f;
+    }
+  } else if constexpr (INTER) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int at = (h == 0 ? ch.c0 : ch.c1) * 2;
+      *reinterpret_cast<float2*>(c + 2 * h) = *reinterpret_cast<const float2*>(cv + at);
+      *reinterpret_cast<float2*>(s + 2 * h) = *reinterpret_cast<const float2*>(sv + at);
+    }
+  } else {
+    *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(cv + ch.c0 * 4);
+    *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(sv + ch.c0 * 4);
   }
 }
 
@@ -238,51 +249,104 @@ __global__ void __launch_bounds__(kThreads, 2) nsa_qk_norm_rope_kernel(const Rop
     }
 }
 
-// Backward. The blocks below `q_blocks` take the query heads, the others the key
-// heads, so that a thread's dw sums belong to one weight. part[block][D]: this
-// block's dw, its lane groups summed in a fixed order.
+// Backward. A thread sums the query weight's gradient of its channels in registers
+// and the key weight's (few heads) in shared memory of its own. part[block]: this
+// block's dw_q and dw_k, its lanes summed in a fixed order.
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kThreads, 2) nsa_qk_norm_rope_bwd_kernel(const RopeBwdArgs b) {
   constexpr int U = D / 64;
   extern __shared__ float4 sm_angles[];   // cosines and sines of each warp's token; at the end the warps' dw
-  __shared__ float4 w_s[D / 4];
+  __shared__ float4 w_s[2][D / 4];
+  __shared__ float4 dwk_s[U][2][kThreads];
   const RopeArgs& a = b.f;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane & (kLanes - 1), grp = lane / kLanes;
   const int half = a.d_rot >> 1, R = a.d_rot >> 2;
   float* cosv = reinterpret_cast<float*>(sm_angles) + warp * a.d_rot;
   float* sinv = cosv + half;
-  const bool is_q = (int)blockIdx.x < b.q_blocks;
-  const int blk = is_q ? blockIdx.x : blockIdx.x - b.q_blocks;
-  const int nblk = is_q ? b.q_blocks : (int)gridDim.x - b.q_blocks;
-  const int H = is_q ? a.H_q : a.H_kv;
-  const float* w = reinterpret_cast<const float*>(w_s);
-  for (int i = threadIdx.x; i < D; i += kThreads) reinterpret_cast<float*>(w_s)[i] = (is_q ? a.w_q : a.w_k)[i];
-  __syncthreads();
-  const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(is_q ? a.q : a.k);
-  const __nv_bfloat16* gb = static_cast<const __nv_bfloat16*>(is_q ? b.dq_out : b.dk_out);
-  __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(is_q ? b.dq : b.dk);
-  const int64_t xs = is_q ? a.q_stride : a.k_stride, os = is_q ? b.dq_stride : b.dk_stride;
-  const int first = (warp % a.wpt) * kWarpHeads + grp, step = a.wpt * kWarpHeads;
+  for (int i = threadIdx.x; i < D; i += kThreads) {
+    reinterpret_cast<float*>(w_s[0])[i] = a.w_q[i];
+    reinterpret_cast<float*>(w_s[1])[i] = a.w_k[i];
+  }
   float dw[U][8];
 #pragma unroll
-  for (int j = 0; j < U; ++j)
+  for (int j = 0; j < U; ++j) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
+    dwk_s[j][0][threadIdx.x] = dwk_s[j][1][threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __syncthreads();
+  const int first = (warp % a.wpt) * kWarpHeads + grp, step = a.wpt * kWarpHeads;
   const int per = kWarps / a.wpt;   // tokens of a block at a time
-#pragma unroll 1
-  for (int64_t n = (int64_t)blk * per + warp / a.wpt; n < a.N; n += (int64_t)nblk * per) {
-    uint2 rx[U][2], rg[U][2];
-    const __nv_bfloat16* x = xb + n * xs;
-    const __nv_bfloat16* g = gb + n * H * D;
-    load_head<U>(x + (int64_t)first * D, first < H, sub, R, rx);
-    load_head<U>(g + (int64_t)first * D, first < H, sub, R, rg);
-    fill_angles(a, n, half, cosv, sinv);
-    float c[U][4], s[U][4];   // the token's angles of this lane's units
+  // one head: cx, cg its channels of x and of the gradient, dst its dx; adds dn h to acc
+  auto head = [&](const uint2 (*cx)[2], const uint2 (*cg)[2], const float* w, bool on, uint2* dst, float (*acc)[8]) {
+    float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < U; ++j) unit_angles<INTER>(unit_chunks(sub + kLanes * j, R), cosv, sinv, c[j], s[j]);
+    for (int j = 0; j < U; ++j) s2 = square_sum(cx[j], s2);
+    const float r = rsqrtf(sum8(s2.x + s2.y) * (1.f / D) + a.eps);
+    const float2 r2 = make_float2(r, r);
+    // dn: the gradient turned back; u = dn w; m = sum(u h), h = x r
+    float u[U][8];
+    float2 m2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const Chunks ch = unit_chunks(sub + kLanes * j, R);
+      float f[8], wv[8];
+      unpack4(cg[j][0], u[j]);
+      unpack4(cg[j][1], u[j] + 4);
+      unpack4(cx[j][0], f);
+      unpack4(cx[j][1], f + 4);
+      if (ch.rot) {
+        float c[4], s[4];
+        unit_angles<INTER>(ch, cosv, sinv, c, s);
+        const float co[4][4] = {{c[0], c[1], c[2], c[3]}, {s[0], s[1], s[2], s[3]},
+                                {-s[0], -s[1], -s[2], -s[3]}, {c[0], c[1], c[2], c[3]}};
+        mix_unit<INTER>(u[j], co);
+      }
+      load_w(w, ch, wv);
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float2 hx = mul2(make_float2(f[i], f[i + 1]), r2), dn = make_float2(u[j][i], u[j][i + 1]);
+        const float2 t = fma2(dn, hx, make_float2(acc[j][i], acc[j][i + 1]));
+        acc[j][i] = t.x;
+        acc[j][i + 1] = t.y;
+        const float2 v = mul2(dn, make_float2(wv[i], wv[i + 1]));
+        m2 = fma2(v, hx, m2);
+        u[j][i] = v.x;
+        u[j][i + 1] = v.y;
+      }
+    }
+    const float m = -sum8(m2.x + m2.y) * (1.f / D) * r;   // -mean(u h) r: h = x r below
+    if (on) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const Chunks ch = unit_chunks(sub + kLanes * j, R);
+        float f[8];
+        unpack4(cx[j][0], f);
+        unpack4(cx[j][1], f + 4);
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {   // r (u - h mean(u h))
+          const float2 v = mul2(r2, fma2(make_float2(f[i], f[i + 1]), make_float2(m, m), make_float2(u[j][i], u[j][i + 1])));
+          f[i] = v.x;
+          f[i + 1] = v.y;
+        }
+        dst[ch.c0] = pack4(f);
+        dst[ch.c1] = pack4(f + 4);
+      }
+    }
+    __syncwarp();
+  };
 #pragma unroll 1
-    for (int h = first; h - grp < H; h += step) {
+  for (int64_t n = (int64_t)blockIdx.x * per + warp / a.wpt; n < a.N; n += (int64_t)gridDim.x * per) {
+    uint2 rx[U][2], rg[U][2];
+    const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.q) + n * a.q_stride;
+    const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(b.dq_out) + n * a.H_q * D;
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(b.dq) + n * b.dq_stride;
+    load_head<U>(x + (int64_t)first * D, first < a.H_q, sub, R, rx);
+    load_head<U>(g + (int64_t)first * D, first < a.H_q, sub, R, rg);
+    fill_angles(a, n, half, cosv, sinv);
+#pragma unroll 1
+    for (int h = first; h - grp < a.H_q; h += step) {
       uint2 cx[U][2], cg[U][2];
 #pragma unroll
       for (int j = 0; j < U; ++j)
@@ -291,96 +355,72 @@ __global__ void __launch_bounds__(kThreads, 2) nsa_qk_norm_rope_bwd_kernel(const
           cx[j][i] = rx[j][i];
           cg[j][i] = rg[j][i];
         }
-      load_head<U>(x + (int64_t)(h + step) * D, h + step < H, sub, R, rx);
-      load_head<U>(g + (int64_t)(h + step) * D, h + step < H, sub, R, rg);
-      float2 s2 = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int j = 0; j < U; ++j) s2 = square_sum(cx[j], s2);
-      const float r = rsqrtf(sum8(s2.x + s2.y) * (1.f / D) + a.eps);
-      const float2 r2 = make_float2(r, r);
-      // dn: the gradient turned back; u = dn w; dw += dn h; m = sum(u h), h = x r
-      float u[U][8];
-      float2 m2 = make_float2(0.f, 0.f);
+      load_head<U>(x + (int64_t)(h + step) * D, h + step < a.H_q, sub, R, rx);
+      load_head<U>(g + (int64_t)(h + step) * D, h + step < a.H_q, sub, R, rg);
+      head(cx, cg, reinterpret_cast<const float*>(w_s[0]), h < a.H_q, reinterpret_cast<uint2*>(o + (int64_t)h * D), dw);
+    }
+    x = static_cast<const __nv_bfloat16*>(a.k) + n * a.k_stride;
+    g = static_cast<const __nv_bfloat16*>(b.dk_out) + n * a.H_kv * D;
+    o = static_cast<__nv_bfloat16*>(b.dk) + n * b.dk_stride;
+#pragma unroll 1
+    for (int h = first; h - grp < a.H_kv; h += step) {
+      load_head<U>(x + (int64_t)h * D, h < a.H_kv, sub, R, rx);
+      load_head<U>(g + (int64_t)h * D, h < a.H_kv, sub, R, rg);
+      float acc[U][8];
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const Chunks ch = unit_chunks(sub + kLanes * j, R);
-        float f[8], wv[8];
-        unpack4(cg[j][0], u[j]);
-        unpack4(cg[j][1], u[j] + 4);
-        unpack4(cx[j][0], f);
-        unpack4(cx[j][1], f + 4);
-        const float co[4][4] = {{c[j][0], c[j][1], c[j][2], c[j][3]},
-                                {s[j][0], s[j][1], s[j][2], s[j][3]},
-                                {-s[j][0], -s[j][1], -s[j][2], -s[j][3]},
-                                {c[j][0], c[j][1], c[j][2], c[j][3]}};
-        mix_unit<INTER>(u[j], co);
-        load_w(w, ch, wv);
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const float2 hx = mul2(make_float2(f[i], f[i + 1]), r2), dn = make_float2(u[j][i], u[j][i + 1]);
-          const float2 t = fma2(dn, hx, make_float2(dw[j][i], dw[j][i + 1]));
-          dw[j][i] = t.x;
-          dw[j][i + 1] = t.y;
-          const float2 v = mul2(dn, make_float2(wv[i], wv[i + 1]));
-          m2 = fma2(v, hx, m2);
-          u[j][i] = v.x;
-          u[j][i + 1] = v.y;
-        }
+        *reinterpret_cast<float4*>(acc[j]) = dwk_s[j][0][threadIdx.x];
+        *reinterpret_cast<float4*>(acc[j] + 4) = dwk_s[j][1][threadIdx.x];
       }
-      const float m = -sum8(m2.x + m2.y) * (1.f / D) * r;   // -mean(u h) r: h = x r below
-      if (h < H) {
-        uint2* dst = reinterpret_cast<uint2*>(ob + n * os + (int64_t)h * D);
+      head(rx, rg, reinterpret_cast<const float*>(w_s[1]), h < a.H_kv, reinterpret_cast<uint2*>(o + (int64_t)h * D), acc);
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-          const Chunks ch = unit_chunks(sub + kLanes * j, R);
-          float f[8];
-          unpack4(cx[j][0], f);
-          unpack4(cx[j][1], f + 4);
-#pragma unroll
-          for (int i = 0; i < 8; i += 2) {   // r (u - h mean(u h))
-            const float2 v = mul2(r2, fma2(make_float2(f[i], f[i + 1]), make_float2(m, m), make_float2(u[j][i], u[j][i + 1])));
-            f[i] = v.x;
-            f[i + 1] = v.y;
-          }
-          dst[ch.c0] = pack4(f);
-          dst[ch.c1] = pack4(f + 4);
-        }
+      for (int j = 0; j < U; ++j) {
+        dwk_s[j][0][threadIdx.x] = *reinterpret_cast<const float4*>(acc[j]);
+        dwk_s[j][1][threadIdx.x] = *reinterpret_cast<const float4*>(acc[j] + 4);
       }
-      __syncwarp();
     }
   }
   // this block's dw: over the 4 lane groups of a warp by shuffles, then over the warps
-  __syncthreads();
   float* red = reinterpret_cast<float*>(sm_angles);   // [8 warps][D]
+#pragma unroll 1
+  for (int role = 0; role < 2; ++role) {
+    if (role == 1) {
 #pragma unroll
-  for (int j = 0; j < U; ++j) {
-    const Chunks ch = unit_chunks(sub + kLanes * j, R);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float t = dw[j][i];
-      t += __shfl_xor_sync(0xffffffffu, t, 8);
-      t += __shfl_xor_sync(0xffffffffu, t, 16);
-      if (lane < kLanes) red[warp * D + (i < 4 ? ch.c0 * 4 + i : ch.c1 * 4 + i - 4)] = t;
+      for (int j = 0; j < U; ++j) {
+        *reinterpret_cast<float4*>(dw[j]) = dwk_s[j][0][threadIdx.x];
+        *reinterpret_cast<float4*>(dw[j] + 4) = dwk_s[j][1][threadIdx.x];
+      }
     }
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < D; e += kThreads) {
-    float t = 0.f;
+    __syncthreads();
 #pragma unroll
-    for (int v = 0; v < kWarps; ++v) t += red[v * D + e];
-    b.part[(size_t)blockIdx.x * D + e] = t;
+    for (int j = 0; j < U; ++j) {
+      const Chunks ch = unit_chunks(sub + kLanes * j, R);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float t = dw[j][i];
+        t += __shfl_xor_sync(0xffffffffu, t, 8);
+        t += __shfl_xor_sync(0xffffffffu, t, 16);
+        if (lane < kLanes) red[warp * D + (i < 4 ? ch.c0 * 4 + i : ch.c1 * 4 + i - 4)] = t;
+      }
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < D; e += kThreads) {
+      float t = 0.f;
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) t += red[v * D + e];
+      b.part[((size_t)blockIdx.x * 2 + role) * D + e] = t;
+    }
   }
 }
 
 // dw = the blocks' parts summed in a fixed order: 32 channels x 8 slices of the
 // blocks per block; grid (D / 32, 2): queries, keys
-__global__ void __launch_bounds__(256) nsa_rope_dw_kernel(const float* part, int q_blocks, int blocks, int D,
-                                                          float* dw_q, float* dw_k) {
+__global__ void __launch_bounds__(256) nsa_rope_dw_kernel(const float* part, int blocks, int D, float* dw_q, float* dw_k) {
   __shared__ float red[8][32];
   const int e = blockIdx.x * 32 + (threadIdx.x & 31), sl = threadIdx.x >> 5;
-  const int lo = blockIdx.y == 0 ? 0 : q_blocks, hi = blockIdx.y == 0 ? q_blocks : blocks;
   float s = 0.f;
-  for (int i = lo + sl; i < hi; i += 8) s += part[(size_t)i * D + e];
+#pragma unroll 8
+  for (int i = sl; i < blocks; i += 8) s += part[((size_t)i * 2 + blockIdx.y) * D + e];
   red[sl][threadIdx.x & 31] = s;
   __syncthreads();
   if (sl == 0) {
@@ -421,21 +461,15 @@ cudaError_t launch_qk_norm_rope(RopeArgs a, int d_k, cudaStream_t st) {
 cudaError_t launch_qk_norm_rope_bwd(RopeBwdArgs b, int d_k, cudaStream_t st) {
   RopeArgs& a = b.f;
   a.wpt = rope_wpt(a.N, a.H_q);
-  // two blocks per SM, dealt to queries and keys by their heads
   const int per = kWarps / a.wpt;
   const int64_t groups = (a.N + per - 1) / per;
-  int kb = (int)((int64_t)kRopeBwdBlocks * a.H_kv / (a.H_q + a.H_kv));
-  if (kb < 1) kb = 1;
-  int qb = kRopeBwdBlocks - kb;
-  if (qb > groups) qb = (int)groups;
-  if (kb > groups) kb = (int)groups;
-  b.q_blocks = qb;
+  const int grid = groups < kRopeBwdBlocks ? (int)groups : kRopeBwdBlocks;
   const size_t ang = (size_t)kWarps * a.d_rot * sizeof(float), red = (size_t)kWarps * d_k * 4;
   const size_t smem = ang > red ? ang : red;
 #define NSA_ROPE(D)                                                                                   \
   case D:                                                                                             \
-    if (a.interleaved) nsa_qk_norm_rope_bwd_kernel<D, true><<<qb + kb, kThreads, smem, st>>>(b);      \
-    else nsa_qk_norm_rope_bwd_kernel<D, false><<<qb + kb, kThreads, smem, st>>>(b);                   \
+    if (a.interleaved) nsa_qk_norm_rope_bwd_kernel<D, true><<<grid, kThreads, smem, st>>>(b);      \
+    else nsa_qk_norm_rope_bwd_kernel<D, false><<<grid, kThreads, smem, st>>>(b);                   \
     break;
   switch (d_k) {
     NSA_ROPE(64)
@@ -446,7 +480,7 @@ cudaError_t launch_qk_norm_rope_bwd(RopeBwdArgs b, int d_k, cudaStream_t st) {
 #undef NSA_ROPE
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  nsa_rope_dw_kernel<<<dim3(d_k / 32, 2), 256, 0, st>>>(b.part, qb, qb + kb, d_k, b.dw_q, b.dw_k);
+  nsa_rope_dw_kernel<<<dim3(d_k / 32, 2), 256, 0, st>>>(b.part, grid, d_k, b.dw_q, b.dw_k);
   return cudaGetLastError();
 }
 
