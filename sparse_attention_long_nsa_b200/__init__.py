@@ -425,40 +425,84 @@ def nsa_dsa_prefill(q, k, v, qi, wi, ki, cu_seqlens, dp: DsaParams, heads: Heads
                                  _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "nsa_dsa_prefill")
 
 
-def _rows(t: torch.Tensor, heads: int, dim: int, name: str) -> tuple:
-    """(pointer, row stride) of bf16 rows [N, heads, dim] whose heads are packed: a
-    whole tensor or a view of a fused projection."""
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-    if t.device.type != "cuda":
+# The entry points of the full-attention layers check shapes, types and devices in few
+# operations per tensor: a decode step's call is shorter than a careless check of it.
+
+def _bad(t, dtype, dev: int, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name}: expected [N, {heads}, {dim}], got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, the call's tensors are on cuda:{dev}")
+    raise ValueError(f"{name}: tensor must be contiguous")
+
+
+def _in(t, dtype, dev: int, shape, name: str):
+    """Device pointer of a contiguous tensor of that type, device and shape."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _bad(t, dtype, dev, name)
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _in_rows(t, dtype, dev: int, n: int, row, name: str):
+    """Likewise of at least n rows of shape `row`."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _bad(t, dtype, dev, name)
+    if t.shape[0] < n or t.shape[1:] != row:
+        raise ValueError(f"{name}: expected [>= {n}, {', '.join(map(str, row))}], got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows(t, n: int, heads: int, dim: int, dev: int, name: str) -> tuple:
+    """(pointer, row stride) of bf16 rows [n, heads, dim] whose heads are packed: a
+    whole tensor or a view of a fused projection."""
+    if t.dtype is not _BF16 or t.get_device() != dev:
+        _bad(t, _BF16, dev, name)
+    if t.shape != (n, heads, dim):
+        raise ValueError(f"{name}: expected shape {(n, heads, dim)}, got {tuple(t.shape)}")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (heads > 1 and s1 != dim):
         raise ValueError(f"{name}: the heads of a token must be packed")
-    return t.data_ptr(), s0 if t.shape[0] > 1 else max(s0, heads * dim)
+    return t.data_ptr(), s0 if n > 1 else max(s0, heads * dim)
 
 
-def _shape(t: Optional[torch.Tensor], shape: tuple, name: str):
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 
 
-def _on(device, stream, *tensors):
-    """The stream of a call whose tensors live on `device`: the given one, or the
-    current stream of that device."""
-    for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device} in one call")
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return _stream(stream)
+def _device_of(t, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    return dev
 
 
-def _device(t: torch.Tensor):
-    """Context that makes the tensor's device current (launches go there)."""
-    return contextlib.nullcontext() if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
+def _raw_stream(dev: int, stream) -> int:
+    """The given stream, or the current one of the tensors' device."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _launch(dev: int, where: str, fn, *args):
+    """Call an entry point with the tensors' device current."""
+    if torch.cuda.current_device() == dev:
+        s = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            s = fn(*args)
+    if s != NSA_OK:
+        _check(s, where)
+
+
+def _ws(ws, dev: int):
+    if ws is None:
+        raise ValueError("ws: a workspace is needed (alloc_workspace of nsa_full_workspace_size bytes)")
+    if ws.get_device() != dev or not ws.is_contiguous():
+        _bad(ws, ws.dtype, dev, "ws")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def nsa_full_workspace_size(op: int, heads: Heads, batch: int, total_tokens: int, max_len: int,
@@ -473,36 +517,29 @@ def nsa_qk_norm_rope(q, k, w_q, w_k, inv_freq, positions, heads: Heads, rope: Ro
     fused projection; w_q, w_k fp32 [d_k]; inv_freq fp32 [d_rot/2]; positions device
     int32 [N]; q_out [N, H_q, d_k]. k_out / v_out [..., H_kv, d]: row n, or row
     cache_rows[n] (device int64 [N]; outside the cache: not written)."""
-    N = int(q.shape[0])
-    qp, qs = _rows(q, heads.H_q, heads.d_k, "q")
-    kp, ks = _rows(k, heads.H_kv, heads.d_k, "k")
-    vp, vs = _rows(v, heads.H_kv, heads.d_v, "v") if v is not None else (None, 0)
-    _shape(k, (N, heads.H_kv, heads.d_k), "k")
+    Hq, Hk, dk, dv, dr = heads.H_q, heads.H_kv, heads.d_k, heads.d_v, rope.d_rot
+    dev, N = _device_of(q, "q"), q.shape[0]
+    qp, qs = _rows(q, N, Hq, dk, dev, "q")
+    kp, ks = _rows(k, N, Hk, dk, dev, "k")
+    if k_out.shape[-2:] != (Hk, dk):
+        raise ValueError(f"k_out: expected [..., {Hk}, {dk}], got {tuple(k_out.shape)}")
+    n_rows = k_out.numel() // (Hk * dk)
+    if (v is None) != (v_out is None):
+        raise ValueError("v and v_out go together")
+    vp = vs = vo = None
     if v is not None:
-        _shape(v, (N, heads.H_kv, heads.d_v), "v")
-    _shape(w_q, (heads.d_k,), "w_q")
-    _shape(w_k, (heads.d_k,), "w_k")
-    _shape(positions, (N,), "positions")
-    _shape(cache_rows, (N,), "cache_rows")
-    if rope.d_rot > 0:
-        _shape(inv_freq, (rope.d_rot // 2,), "inv_freq")
-    _shape(q_out, (N, heads.H_q, heads.d_k), "q_out")
-    if tuple(k_out.shape[-2:]) != (heads.H_kv, heads.d_k):
-        raise ValueError(f"k_out: expected [..., {heads.H_kv}, {heads.d_k}], got {tuple(k_out.shape)}")
-    n_rows = k_out.numel() // (heads.H_kv * heads.d_k)
-    if v_out is not None and (tuple(v_out.shape[-2:]) != (heads.H_kv, heads.d_v) or
-                              v_out.numel() != n_rows * heads.H_kv * heads.d_v):
-        raise ValueError("v_out must have the rows of k_out")
-    st = _on(q.device, stream, k, v, w_q, w_k, inv_freq, positions, cache_rows, q_out, k_out, v_out)
-    if N == 0:
-        return
-    with _device(q):
-        s = lib().nsa_qk_norm_rope(qp, qs, kp, ks, vp, vs, _ptr(w_q, torch.float32), _ptr(w_k, torch.float32),
-                                   _ptr(inv_freq, torch.float32) if rope.d_rot > 0 else None,
-                                   _ptr(positions, torch.int32), _ptr(cache_rows, torch.int64), n_rows, N,
-                                   ctypes.byref(heads), ctypes.byref(rope), _ptr(q_out, torch.bfloat16),
-                                   _ptr(k_out, torch.bfloat16), _ptr(v_out, torch.bfloat16), st)
-    _check(s, "nsa_qk_norm_rope")
+        vp, vs = _rows(v, N, Hk, dv, dev, "v")
+        if v_out.shape[-2:] != (Hk, dv) or v_out.numel() != n_rows * Hk * dv:
+            raise ValueError(f"v_out: expected [..., {Hk}, {dv}] with the rows of k_out, got {tuple(v_out.shape)}")
+        vo = _in(v_out, _BF16, dev, v_out.shape, "v_out")
+    args = (qp, qs, kp, ks, vp, vs or 0, _in(w_q, _F32, dev, (dk,), "w_q"), _in(w_k, _F32, dev, (dk,), "w_k"),
+            _in(inv_freq, _F32, dev, (dr // 2,), "inv_freq") if dr > 0 else None,
+            _in(positions, _I32, dev, (N,), "positions"),
+            None if cache_rows is None else _in(cache_rows, _I64, dev, (N,), "cache_rows"), n_rows, N,
+            ctypes.byref(heads), ctypes.byref(rope), _in(q_out, _BF16, dev, (N, Hq, dk), "q_out"),
+            _in(k_out, _BF16, dev, k_out.shape, "k_out"), vo, _raw_stream(dev, stream))
+    if N > 0:   # empty tensors have no address
+        _launch(dev, "nsa_qk_norm_rope", lib().nsa_qk_norm_rope, *args)
 
 
 def nsa_qk_norm_rope_backward(q, k, w_q, w_k, inv_freq, positions, dq_out, dk_out, heads: Heads, rope: RopeParams, dq,
@@ -510,99 +547,68 @@ def nsa_qk_norm_rope_backward(q, k, w_q, w_k, inv_freq, positions, dq_out, dk_ou
     """Gradients of nsa_qk_norm_rope: dq_out, dk_out bf16 (of its outputs, packed) in;
     dq, dk bf16 [N, H, d_k] (packed or views of a fused gradient) and dw_q, dw_k fp32
     [d_k] out."""
-    N = int(q.shape[0])
-    qp, qs = _rows(q, heads.H_q, heads.d_k, "q")
-    kp, ks = _rows(k, heads.H_kv, heads.d_k, "k")
-    gqp, gqs = _rows(dq, heads.H_q, heads.d_k, "dq")
-    gkp, gks = _rows(dk, heads.H_kv, heads.d_k, "dk")
-    for t, name, h in ((k, "k", heads.H_kv), (dq, "dq", heads.H_q), (dk, "dk", heads.H_kv),
-                       (dq_out, "dq_out", heads.H_q), (dk_out, "dk_out", heads.H_kv)):
-        _shape(t, (N, h, heads.d_k), name)
-    for t, name in ((w_q, "w_q"), (w_k, "w_k"), (dw_q, "dw_q"), (dw_k, "dw_k")):
-        _shape(t, (heads.d_k,), name)
-    _shape(positions, (N,), "positions")
-    if rope.d_rot > 0:
-        _shape(inv_freq, (rope.d_rot // 2,), "inv_freq")
-    f32 = torch.float32
-    st = _on(q.device, stream, k, w_q, w_k, inv_freq, positions, dq_out, dk_out, dq, dk, dw_q, dw_k, ws)
-    if N == 0:   # empty tensors have no address
-        if stream is None:
+    Hq, Hk, d, dr = heads.H_q, heads.H_kv, heads.d_k, rope.d_rot
+    dev, N = _device_of(q, "q"), q.shape[0]
+    qp, qs = _rows(q, N, Hq, d, dev, "q")
+    kp, ks = _rows(k, N, Hk, d, dev, "k")
+    gqp, gqs = _rows(dq, N, Hq, d, dev, "dq")
+    gkp, gks = _rows(dk, N, Hk, d, dev, "dk")
+    st = _raw_stream(dev, stream)
+    args = (qp, qs, kp, ks, _in(w_q, _F32, dev, (d,), "w_q"), _in(w_k, _F32, dev, (d,), "w_k"),
+            _in(inv_freq, _F32, dev, (dr // 2,), "inv_freq") if dr > 0 else None,
+            _in(positions, _I32, dev, (N,), "positions"), N, _in(dq_out, _BF16, dev, (N, Hq, d), "dq_out"),
+            _in(dk_out, _BF16, dev, (N, Hk, d), "dk_out"), ctypes.byref(heads), ctypes.byref(rope), gqp, gqs, gkp,
+            gks, _in(dw_q, _F32, dev, (d,), "dw_q"), _in(dw_k, _F32, dev, (d,), "dw_k"), *_ws(ws, dev), st)
+    if N > 0:
+        _launch(dev, "nsa_qk_norm_rope_backward", lib().nsa_qk_norm_rope_backward, *args)
+    else:       # empty tensors have no address; the sums over no tokens
+        with torch.cuda.stream(torch.cuda.ExternalStream(st, device=q.device)):
             dw_q.zero_()
             dw_k.zero_()
-        else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(st, device=q.device)):
-                dw_q.zero_()
-                dw_k.zero_()
-        return
-    with _device(q):
-        s = lib().nsa_qk_norm_rope_backward(
-            qp, qs, kp, ks, _ptr(w_q, f32), _ptr(w_k, f32), _ptr(inv_freq, f32) if rope.d_rot > 0 else None,
-            _ptr(positions, torch.int32), N, _ptr(dq_out, torch.bfloat16), _ptr(dk_out, torch.bfloat16),
-            ctypes.byref(heads), ctypes.byref(rope), gqp, gqs, gkp, gks, _ptr(dw_q, f32), _ptr(dw_k, f32), _ptr(ws),
-            ws.numel() * ws.element_size(), st)
-    _check(s, "nsa_qk_norm_rope_backward")
 
 
-def _check_packed(q, k, v, cu_seqlens, heads: Heads):
-    """Shapes of packed prompts against cu_seqlens (host int32 [B + 1])."""
-    B = int(cu_seqlens.numel()) - 1
+def _batch_of(cu_seqlens) -> tuple:
+    """(pointer, batch, rows) of host int32 cu_seqlens."""
+    if cu_seqlens.dtype is not _I32 or cu_seqlens.is_cuda or not cu_seqlens.is_contiguous() or cu_seqlens.dim() != 1:
+        raise ValueError("cu_seqlens: expected a host int32 tensor [batch + 1]")
+    B = cu_seqlens.shape[0] - 1
     if B < 1:
         raise ValueError("cu_seqlens needs at least two entries")
-    N = int(cu_seqlens[-1])
-    for t, name, shape in ((q, "q", (heads.H_q, heads.d_k)), (k, "k", (heads.H_kv, heads.d_k)),
-                           (v, "v", (heads.H_kv, heads.d_v))):
-        if t.dim() != 3 or t.shape[0] < N or tuple(t.shape[1:]) != shape:
-            raise ValueError(f"{name}: expected [>= {N}, {shape[0]}, {shape[1]}], got {tuple(t.shape)}")
-    return B, N
+    return cu_seqlens.data_ptr(), B, int(cu_seqlens[-1])
 
 
 def nsa_full_prefill(q, k, v, cu_seqlens, heads: Heads, out, lse_out=None, ws=None, scale: float = 0.0, stream=None):
     """Causal full attention over packed prompts; cu_seqlens host int32 [B+1];
-    out bf16 [N, H_q, d_v]; lse_out fp32 [N, H_q] or None."""
-    B, N = _check_packed(q, k, v, cu_seqlens, heads)
-    if out.dim() != 3 or out.shape[0] < N or tuple(out.shape[1:]) != (heads.H_q, heads.d_v):
-        raise ValueError(f"out: expected [>= {N}, {heads.H_q}, {heads.d_v}], got {tuple(out.shape)}")
-    if lse_out is not None and (lse_out.dim() != 2 or lse_out.shape[0] < N or lse_out.shape[1] != heads.H_q):
-        raise ValueError(f"lse_out: expected [>= {N}, {heads.H_q}], got {tuple(lse_out.shape)}")
-    st = _on(q.device, stream, k, v, out, lse_out, ws)
-    with _device(q):
-        s = lib().nsa_full_prefill(_ptr(q, torch.bfloat16), _ptr(k, torch.bfloat16), _ptr(v, torch.bfloat16),
-                                   _ptr(cu_seqlens, torch.int32, "cpu"), B, ctypes.byref(heads), float(scale),
-                                   _ptr(out, torch.bfloat16), _ptr(lse_out, torch.float32), _ptr(ws),
-                                   ws.numel() * ws.element_size(), st)
-    _check(s, "nsa_full_prefill")
+    out bf16 [N, H_q, d_v]; lse_out fp32 [N, H_q] or None. Tensors may have more rows
+    than cu_seqlens[B]."""
+    Hq, Hk, dk, dv = heads.H_q, heads.H_kv, heads.d_k, heads.d_v
+    cu, B, N = _batch_of(cu_seqlens)
+    dev = _device_of(q, "q")
+    if N == 0:   # empty tensors have no address
+        return
+    _launch(dev, "nsa_full_prefill", lib().nsa_full_prefill, _in_rows(q, _BF16, dev, N, (Hq, dk), "q"),
+            _in_rows(k, _BF16, dev, N, (Hk, dk), "k"), _in_rows(v, _BF16, dev, N, (Hk, dv), "v"), cu, B,
+            ctypes.byref(heads), scale, _in_rows(out, _BF16, dev, N, (Hq, dv), "out"),
+            None if lse_out is None else _in_rows(lse_out, _F32, dev, N, (Hq,), "lse_out"), *_ws(ws, dev),
+            _raw_stream(dev, stream))
 
 
 def nsa_full_prefill_backward(q, k, v, out, lse, dout, cu_seqlens, heads: Heads, dq, dk, dv, ws, scale: float = 0.0,
                               stream=None):
     """Gradients of nsa_full_prefill from its inputs, out, lse_out and dout bf16
     [N, H_q, d_v]: dq, dk, dv bf16, the shapes of q, k, v."""
-    B, N = _check_packed(q, k, v, cu_seqlens, heads)
-    for t, name, shape in ((out, "out", (heads.H_q, heads.d_v)), (dout, "dout", (heads.H_q, heads.d_v)),
-                           (lse, "lse", (heads.H_q,)), (dq, "dq", (heads.H_q, heads.d_k)),
-                           (dk, "dk", (heads.H_kv, heads.d_k)), (dv, "dv", (heads.H_kv, heads.d_v))):
-        if t.dim() != 1 + len(shape) or t.shape[0] < N or tuple(t.shape[1:]) != shape:
-            raise ValueError(f"{name}: expected [>= {N}, ...] with {shape}, got {tuple(t.shape)}")
-    st = _on(q.device, stream, k, v, out, lse, dout, dq, dk, dv, ws)
-    bf = torch.bfloat16
-    with _device(q):
-        s = lib().nsa_full_prefill_backward(_ptr(q, bf), _ptr(k, bf), _ptr(v, bf), _ptr(out, bf),
-                                            _ptr(lse, torch.float32), _ptr(dout, bf),
-                                            _ptr(cu_seqlens, torch.int32, "cpu"), B, ctypes.byref(heads),
-                                            float(scale), _ptr(dq, bf), _ptr(dk, bf), _ptr(dv, bf), _ptr(ws),
-                                            ws.numel() * ws.element_size(), st)
-    _check(s, "nsa_full_prefill_backward")
-
-
-def _check_tree(q, cache_lens, n_nodes, tree_mask, heads: Heads, out, lse_out):
-    B, M = int(q.shape[0]), int(q.shape[1])
-    _shape(q, (B, M, heads.H_q, heads.d_k), "q")
-    _shape(cache_lens, (B,), "cache_lens")
-    _shape(n_nodes, (B,), "n_nodes")
-    _shape(tree_mask, (B, M), "tree_mask")
-    _shape(out, (B, M, heads.H_q, heads.d_v), "out")
-    _shape(lse_out, (B, M, heads.H_q), "lse_out")
-    return B, M
+    Hq, Hk, d, e = heads.H_q, heads.H_kv, heads.d_k, heads.d_v
+    cu, B, N = _batch_of(cu_seqlens)
+    dev = _device_of(q, "q")
+    if N == 0:
+        return
+    _launch(dev, "nsa_full_prefill_backward", lib().nsa_full_prefill_backward,
+            _in_rows(q, _BF16, dev, N, (Hq, d), "q"), _in_rows(k, _BF16, dev, N, (Hk, d), "k"),
+            _in_rows(v, _BF16, dev, N, (Hk, e), "v"), _in_rows(out, _BF16, dev, N, (Hq, e), "out"),
+            _in_rows(lse, _F32, dev, N, (Hq,), "lse"), _in_rows(dout, _BF16, dev, N, (Hq, e), "dout"), cu, B,
+            ctypes.byref(heads), scale, _in_rows(dq, _BF16, dev, N, (Hq, d), "dq"),
+            _in_rows(dk, _BF16, dev, N, (Hk, d), "dk"), _in_rows(dv, _BF16, dev, N, (Hk, e), "dv"), *_ws(ws, dev),
+            _raw_stream(dev, stream))
 
 
 def nsa_full_tree_decode(q, k_cache, v_cache, cache_lens, n_nodes, tree_mask, max_len: int, heads: Heads, out,
@@ -611,40 +617,53 @@ def nsa_full_tree_decode(q, k_cache, v_cache, cache_lens, n_nodes, tree_mask, ma
     that hold the nodes as their last n_nodes[b] tokens; cache_lens, n_nodes (or None)
     device int32 [B]; tree_mask device int64 [B, M], bit j of word i: node i sees node
     j (None: a chain)."""
-    B, M = _check_tree(q, cache_lens, n_nodes, tree_mask, heads, out, lse_out)
-    Lmax = int(k_cache.shape[1])
-    _shape(k_cache, (B, Lmax, heads.H_kv, heads.d_k), "k_cache")
-    _shape(v_cache, (B, Lmax, heads.H_kv, heads.d_v), "v_cache")
-    st = _on(q.device, stream, k_cache, v_cache, cache_lens, n_nodes, tree_mask, out, lse_out, ws)
-    with _device(q):
-        s = lib().nsa_full_tree_decode(_ptr(q, torch.bfloat16), _ptr(k_cache, torch.bfloat16),
-                                       _ptr(v_cache, torch.bfloat16), _ptr(cache_lens, torch.int32),
-                                       _ptr(n_nodes, torch.int32), _ptr(tree_mask, torch.int64), B, M, Lmax,
-                                       int(max_len), ctypes.byref(heads), float(scale), _ptr(out, torch.bfloat16),
-                                       _ptr(lse_out, torch.float32), _ptr(ws), ws.numel() * ws.element_size(), st)
-    _check(s, "nsa_full_tree_decode")
+    Hq, Hk, dk, dv = heads.H_q, heads.H_kv, heads.d_k, heads.d_v
+    dev = _device_of(q, "q")
+    B, M, Lmax = q.shape[0], q.shape[1], k_cache.shape[1]
+    _launch(dev, "nsa_full_tree_decode", lib().nsa_full_tree_decode, _in(q, _BF16, dev, (B, M, Hq, dk), "q"),
+            _in(k_cache, _BF16, dev, (B, Lmax, Hk, dk), "k_cache"),
+            _in(v_cache, _BF16, dev, (B, Lmax, Hk, dv), "v_cache"), _in(cache_lens, _I32, dev, (B,), "cache_lens"),
+            None if n_nodes is None else _in(n_nodes, _I32, dev, (B,), "n_nodes"),
+            None if tree_mask is None else _in(tree_mask, _I64, dev, (B, M), "tree_mask"), B, M, Lmax, max_len,
+            ctypes.byref(heads), scale, _in(out, _BF16, dev, (B, M, Hq, dv), "out"),
+            None if lse_out is None else _in(lse_out, _F32, dev, (B, M, Hq), "lse_out"), *_ws(ws, dev),
+            _raw_stream(dev, stream))
 
 
 def nsa_full_tree_decode_paged(q, k_pool, v_pool, block_table, cache_lens, n_nodes, tree_mask, max_len: int,
                                heads: Heads, out, lse_out=None, ws=None, scale: float = 0.0, stream=None):
     """nsa_full_tree_decode over pools [n_pages, page_size, H_kv, d] and a device int32
     block_table [B, max_pages]."""
-    B, M = _check_tree(q, cache_lens, n_nodes, tree_mask, heads, out, lse_out)
-    pages, size = int(k_pool.shape[0]), int(k_pool.shape[1])
-    _shape(k_pool, (pages, size, heads.H_kv, heads.d_k), "k_pool")
-    _shape(v_pool, (pages, size, heads.H_kv, heads.d_v), "v_pool")
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table: expected [{B}, max_pages], got {tuple(block_table.shape)}")
-    st = _on(q.device, stream, k_pool, v_pool, block_table, cache_lens, n_nodes, tree_mask, out, lse_out, ws)
-    with _device(q):
-        s = lib().nsa_full_tree_decode_paged(_ptr(q, torch.bfloat16), _ptr(k_pool, torch.bfloat16),
-                                             _ptr(v_pool, torch.bfloat16), pages, size,
-                                             _ptr(block_table, torch.int32), int(block_table.shape[1]),
-                                             _ptr(cache_lens, torch.int32), _ptr(n_nodes, torch.int32),
-                                             _ptr(tree_mask, torch.int64), B, M, int(max_len), ctypes.byref(heads),
-                                             float(scale), _ptr(out, torch.bfloat16), _ptr(lse_out, torch.float32),
-                                             _ptr(ws), ws.numel() * ws.element_size(), st)
-    _check(s, "nsa_full_tree_decode_paged")
+    Hq, Hk, dk, dv = heads.H_q, heads.H_kv, heads.d_k, heads.d_v
+    dev = _device_of(q, "q")
+    B, M, pages, size, cols = q.shape[0], q.shape[1], k_pool.shape[0], k_pool.shape[1], block_table.shape[-1]
+    _launch(dev, "nsa_full_tree_decode_paged", lib().nsa_full_tree_decode_paged,
+            _in(q, _BF16, dev, (B, M, Hq, dk), "q"), _in(k_pool, _BF16, dev, (pages, size, Hk, dk), "k_pool"),
+            _in(v_pool, _BF16, dev, (pages, size, Hk, dv), "v_pool"), pages, size,
+            _in(block_table, _I32, dev, (B, cols), "block_table"), cols,
+            _in(cache_lens, _I32, dev, (B,), "cache_lens"),
+            None if n_nodes is None else _in(n_nodes, _I32, dev, (B,), "n_nodes"),
+            None if tree_mask is None else _in(tree_mask, _I64, dev, (B, M), "tree_mask"), B, M, max_len,
+            ctypes.byref(heads), scale, _in(out, _BF16, dev, (B, M, Hq, dv), "out"),
+            None if lse_out is None else _in(lse_out, _F32, dev, (B, M, Hq), "lse_out"), *_ws(ws, dev),
+            _raw_stream(dev, stream))
+
+
+def tree_mask_from_parents(parents: torch.Tensor) -> torch.Tensor:
+    """The tree_mask of nsa_full_tree_decode from parents [B, M] (integer; parents[b, i]
+    < i is the node that node i continues, -1: none): int64 [B, M] on the same device,
+    each node's ancestors and itself."""
+    B, M = parents.shape
+    if M > NSA_MAX_NODES:
+        raise ValueError(f"at most {NSA_MAX_NODES} nodes, got {M}")
+    p = parents.to(torch.int64)
+    if bool((p >= torch.arange(M, device=p.device)).any()) or bool((p < -1).any()):
+        raise ValueError("a node's parent must be an earlier node or -1")
+    words = torch.zeros((B, M + 1), dtype=torch.int64, device=p.device)   # word M: of no node
+    for i in range(M):
+        words[:, i] = words.gather(1, torch.where(p[:, i] < 0, M, p[:, i]).unsqueeze(1)).squeeze(1)
+        words[:, i] |= 1 << i if i < 63 else -(1 << 63)
+    return words[:, :M].contiguous()
 
 
 def nsa_profile_enable(enable: bool):
