@@ -211,10 +211,13 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait();
+  pdl_launch_dependents();
   const uint32_t tmem = bars->tmem_base;
   const int TOK = kRows / a.G;
   KvSched sched(a);
   KvSeg sg;
+  sg.slot = -1;
   bool ok = true;
   auto uwait = [&](uint64_t* bar, uint32_t parity, uint32_t site) -> bool {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, abort_flag, a.status, site));
@@ -489,50 +492,68 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
       tc_fence_before();   // the next unit's products wait for this thread's next arrivals
     }
   }
+  if (tid == 0) {   // for the merge: {sequence, key head, key block, last run} of the unit cut by this run's end
+    int4 cut = make_int4(-1, 0, 0, 0);
+    if (sg.slot == 2 * (int)blockIdx.x + 1) {
+      const int blocks = gridDim.x;
+      const int64_t end = run_begin(a, blockIdx.x + 1, blocks) - sg.n + ((sg.L + TOK - 1) / TOK - sg.kt * a.G);
+      int c1 = blockIdx.x + 1;
+      while (c1 + 1 < blocks && run_begin(a, c1 + 1, blocks) < end) ++c1;
+      cut = make_int4(sg.b, sg.g, sg.kt, c1);
+    }
+    a.cut[blockIdx.x] = cut;
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
-// The units that a border between runs cut: their parts in block order. Block x:
-// the unit that begins in run x and ends beyond it, 8 keys per block of threads.
+// The units that a border between runs cut: their parts in block order. Block x: the
+// unit that begins in run x and ends beyond it, if there is one; a warp takes four keys.
 template <int DK, int DV>
-__global__ void __launch_bounds__(256) nsa_full_bwd_merge_kernel(const FullBwdArgs a, int blocks) {
+__global__ void __launch_bounds__(256) nsa_full_bwd_merge_kernel(const FullBwdArgs a) {
   constexpr int E = (DK + DV) / 64;   // pairs of channels per lane
+  pdl_wait();   // every block of a kernel in a chain of early launches waits, before any exit
   const int c0 = blockIdx.x;
-  const int64_t lo = run_begin(a, c0, blocks), hi = run_begin(a, c0 + 1, blocks);
-  if (lo >= hi) return;
-  const KvPlace p = kv_place(a, hi - 1);
-  const int64_t end = p.start + p.cnt;
-  if (p.start < lo || end <= hi) return;
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int key = p.kt * kRows + r;
-  if (key >= a.len[p.b]) return;
-  float2 s[E];
+  const int4 cut = a.cut[c0];
+  if (cut.x < 0) return;
+  const int lane = threadIdx.x & 31, r0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * 4;
+  const int have = min(a.len[cut.x] - cut.z * kRows, kRows);   // keys of the block
+  if (r0 >= have) return;
+  const int64_t ld = (int64_t)kRows * (DK + DV);
+  float2 s[4][E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) s[e] = make_float2(0.f, 0.f);
-  for (int c = c0; c < blocks; ++c) {
-    const int64_t b0 = run_begin(a, c, blocks), b1 = run_begin(a, c + 1, blocks);
-    if (b0 >= end) break;
-    if (b0 == b1) continue;
-    const float2* src = reinterpret_cast<const float2*>(
-        a.part + ((int64_t)(2 * c + (c == c0 ? 1 : 0)) * kRows + r) * (DK + DV));
+  for (int k = 0; k < 4; ++k)
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float2 v = src[e * 32 + lane];
-      s[e].x += v.x;
-      s[e].y += v.y;
+    for (int e = 0; e < E; ++e) s[k][e] = make_float2(0.f, 0.f);
+#pragma unroll 2
+  for (int c = c0; c <= cut.w; ++c) {
+    const float* slot = a.part + (2 * c + (c == c0 ? 1 : 0)) * ld;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2* src = reinterpret_cast<const float2*>(slot + (int64_t)min(r0 + k, have - 1) * (DK + DV));
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float2 v = src[e * 32 + lane];
+        s[k][e].x += v.x;
+        s[k][e].y += v.y;
+      }
     }
   }
-  const int64_t row = (a.tok_off[p.b] + key) * a.H_kv + p.g;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {   // channels 0 .. DV - 1: dV, then dK
-    const int ch = e * 64 + lane * 2;
-    if (e * 64 < DV)
-      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.dv) + row * DV + ch) = pack_bf16x2(s[e].x, s[e].y);
-    else
-      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.dk) + row * DK + ch - DV) =
-          pack_bf16x2(s[e].x * a.scale, s[e].y * a.scale);
+  for (int k = 0; k < 4; ++k) {
+    if (r0 + k >= have) break;
+    const int64_t row = (a.tok_off[cut.x] + cut.z * kRows + r0 + k) * a.H_kv + cut.y;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {   // channels 0 .. DV - 1: dV, then dK
+      const int ch = e * 64 + lane * 2;
+      if (e * 64 < DV)
+        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.dv) + row * DV + ch) =
+            pack_bf16x2(s[k][e].x, s[k][e].y);
+      else
+        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.dk) + row * DK + ch - DV) =
+            pack_bf16x2(s[k][e].x * a.scale, s[k][e].y * a.scale);
+    }
   }
 }
 
@@ -557,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_q_kernel(const FullB
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait();
   const uint32_t tmem = bars->tmem_base;
   const int TOK = kRows / a.G;
   bool ok = true;
@@ -809,13 +831,16 @@ static cudaError_t launch_bwd_t(const FullBwdArgs& a, const FullBwdMaps& m, cuda
   cudaError_t e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int64_t threads = a.n_rows * (DV / 8);
+  const int64_t threads = a.n_rows * (DV / 8), W = a.kv_prefix[a.batch];
   nsa_full_bwd_row_kernel<DV><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a);
-  kv<<<kFullBlocks, kThreads, smem, st>>>(a, m);
-  nsa_full_bwd_merge_kernel<DK, DV><<<dim3(kFullBlocks, kRows / 8), 256, 0, st>>>(a, kFullBlocks);
+  const int runs = W < kFullBlocks ? (int)W : kFullBlocks;
   const int grid = a.n_items < kFullBlocks ? (int)a.n_items : kFullBlocks;
-  kq<<<grid, kThreads, smem, st>>>(a, m);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e == cudaSuccess) e = launch_after(kv, dim3(runs), kThreads, smem, st, a, m);
+  if (e == cudaSuccess)
+    e = launch_after(nsa_full_bwd_merge_kernel<DK, DV>, dim3(runs, kRows / 32), 256, 0, st, a);
+  if (e == cudaSuccess) e = launch_after(kq, dim3(grid), kThreads, smem, st, a, m);
+  return e;
 }
 
 cudaError_t launch_full_bwd(const FullBwdArgs& a, const FullBwdMaps& m, int d_k, int d_v, cudaStream_t st) {

@@ -126,9 +126,9 @@ struct TreeSched {
   const int* prefix;   // [B + 1] key tiles of the sequences before
   int pos, end, b = 0;
   __device__ TreeSched(const FullArgs& a_, const int* p) : a(a_), prefix(p) {
-    const int64_t W = p[a.B], c = blockIdx.x, n = gridDim.x;
-    pos = (int)(W * c / n);
-    end = (int)(W * (c + 1) / n);
+    const int64_t W = p[a.B], c = blockIdx.x, n = min((int64_t)gridDim.x, W);   // every run has tiles
+    pos = c < n ? (int)(W * c / n) : 0;
+    end = c < n ? (int)(W * (c + 1) / n) : 0;
   }
   __device__ bool next(FaSeg& s) {
     if (pos >= end) return false;
@@ -245,8 +245,10 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  if (TREE) pdl_launch_dependents();   // the merge may be scheduled; it waits for this grid's end
   FaSched<NT, TREE> sched(a, prefix);
   FaSeg sg;
+  sg.slot = -1;
   bool ok = true;
 
   if (warp == 16) {
@@ -673,8 +675,16 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
     }
   }
 
-  if (TREE && blockIdx.x == 0 && tid < 32) {
-    for (int i = lane; i <= a.B; i += 32) a.prefix_out[i] = prefix[i];
+  if (TREE && tid == 0) {
+    // for the merge: {sequence, key head, first row's node, last run} of the unit that
+    // begins in this run and ends beyond it; sequence -1: none
+    int4 cut = make_int4(-1, 0, 0, 0);
+    if (sg.slot == 2 * (int)blockIdx.x + 1) {
+      const int64_t W = prefix[a.B], nb = min((int64_t)gridDim.x, W);
+      const int64_t end = W * (blockIdx.x + 1) / nb - sg.nt[0] + (sg.nkeys + kFaKeys - 1) / kFaKeys;   // behind the unit
+      cut = make_int4(sg.b, sg.g, sg.i0, (int)((end * nb - 1) / W));
+    }
+    a.cut[blockIdx.x] = cut;
   }
   tc_fence_before();
   __syncthreads();

@@ -231,6 +231,24 @@ struct RopeBwdArgs {
 cudaError_t launch_qk_norm_rope(RopeArgs a, int d_k, cudaStream_t st);
 cudaError_t launch_qk_norm_rope_bwd(RopeBwdArgs b, int d_k, cudaStream_t st);
 
+// A launch whose blocks may be scheduled while the kernel before it on the stream
+// still runs; the kernel waits with pdl_wait() before it reads that one's results
+// (and its predecessors': each kernel of such a chain waits).
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
 // ----- full attention -----
 constexpr int kFullBlocks = 148;      // one persistent block per SM
 struct FullArgs {
@@ -250,7 +268,7 @@ struct FullArgs {
   int B, M, Lmax, max_len;
   PageTable pt;
   float* part;            // partial results [2 * kFullBlocks][rows][d_v + 4]: O, max (log2 units), sum
-  int32_t* prefix_out;    // [B + 1] key tiles of the sequences before, for the merge
+  int4* cut;              // [kFullBlocks] the unit that a run's end cuts, for the merge
 };
 struct FullMaps {
   CUtensorMap q;          // box of 128/G tokens x G heads x 64 channels
@@ -268,6 +286,7 @@ struct FullBwdArgs {
   float2* row;            // [N, H_q] (lse in log2 units, delta)
   void *dq, *dk, *dv;     // bf16
   float* part;            // partial dV, dK of the cut units [2 * kFullBlocks][128][d_v + d_k]
+  int4* cut;              // [kFullBlocks] the unit that a run's end cuts, for the merge
   int H_q, H_kv, G, batch;
   float scale, scale_log2;
   uint32_t* status;

@@ -1132,24 +1132,25 @@ int64_t fill_levels(SeqTable& t, const int32_t* cu_seqlens, int batch, int tok) 
 }
 
 struct TreeWs {
-  size_t prefix, part, total;
+  size_t cut, part, total;
 };
 TreeWs tree_ws(const nsa_heads_t* h, int max_nodes) {
   TreeWs w{};
   size_t off = 256;
-  w.prefix = off; off = align256(off + (NSA_MAX_BATCH + 1) * 4);
+  w.cut = off; off = align256(off + kFullBlocks * sizeof(int4));
   w.part = off; off = align256(off + full_part_bytes(max_nodes * (h->H_q / h->H_kv) > 128 ? 2 : 1, h->d_v));
   w.total = off;
   return w;
 }
 
 struct FullBwdWs {
-  size_t row, part, total;
+  size_t row, cut, part, total;
 };
 FullBwdWs full_bwd_ws(const nsa_heads_t* h, int64_t N) {
   FullBwdWs w{};
   size_t off = 256;
   w.row = off; off = align256(off + (size_t)N * h->H_q * 8);
+  w.cut = off; off = align256(off + kFullBlocks * sizeof(int4));
   w.part = off; off = align256(off + (size_t)2 * kFullBlocks * 128 * (h->d_k + h->d_v) * 4);
   w.total = off;
   return w;
@@ -1197,7 +1198,7 @@ nsa_status_t tree_common(const void* q, const void* k, const void* v, const int3
   a.mask = tree_mask;
   a.B = batch; a.M = max_nodes; a.Lmax = Lmax; a.max_len = max_len;
   a.pt = pt;
-  a.prefix_out = (int32_t*)(ws + w.prefix);
+  a.cut = (int4*)(ws + w.cut);
   a.part = (float*)(ws + w.part);
   FullMaps m;
   memset(&m, 0, sizeof(m));
@@ -1371,6 +1372,7 @@ nsa_status_t nsa_full_prefill_backward(const void* q, const void* k, const void*
   a.out = out; a.dout = dout; a.lse = lse; a.dq = dq; a.dk = dk; a.dv = dv;
   a.row = (float2*)(ws + w.row);
   a.part = (float*)(ws + w.part);
+  a.cut = (int4*)(ws + w.cut);
   a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)heads->d_k);
   a.scale_log2 = a.scale * 1.4426950408889634f;
   a.status = reinterpret_cast<uint32_t*>(ws);
