@@ -23,8 +23,10 @@ extern "C" {
 #endif
 
 /* Sites: 0 = none; 1 = the decode fine pass withholds its first key tile;
- * 2 = the prefill kernel withholds its first key tile. Applies to every later
- * nsa_prefill / nsa_decode call of this process until set back to 0. Returns
+ * 2 = the prefill kernel withholds its first key tile; 3 = the full-attention
+ * kernel (prompts and drafted tokens) withholds its first key tile; 4 = the key side
+ * of its backward withholds its first row tile. Applies to every later call of this
+ * process until set back to 0. Returns
  * NSA_ERR_INVALID_ARG for an unknown site. Host-only (no GPU work). */
 nsa_status_t nsa_test_set_fault(int32_t site);
 

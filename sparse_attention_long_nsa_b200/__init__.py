@@ -44,7 +44,7 @@ NSA_OP_FULL_PREFILL, NSA_OP_FULL_BACKWARD, NSA_OP_TREE_DECODE, NSA_OP_ROPE_BACKW
 NSA_MAX_NODES = 64
 # the checking build exports one more symbol (include/nsa_check.h)
 CHECK_EXPORTED = EXPORTED + ("nsa_test_set_fault",)
-FAULT_NONE, FAULT_DECODE_FINE_TILE, FAULT_PREFILL_K_TILE = 0, 1, 2
+FAULT_NONE, FAULT_DECODE_FINE_TILE, FAULT_PREFILL_K_TILE, FAULT_FULL_TILE, FAULT_FULL_BWD_TILE = range(5)
 
 
 class NSAError(RuntimeError):

@@ -54,7 +54,8 @@ __device__ __forceinline__ bool bounds_ok(bool cond, uint32_t* status, uint32_t 
 // site; the producer named by it withholds one tile, so the waits on that tile
 // run out (bounded, NSA_WAIT_LIMIT_NS) and the kernel records DEV_ERR_TIMEOUT and
 // returns. Nothing is injected in the library build.
-enum : int { FAULT_NONE = 0, FAULT_DECODE_FINE_TILE = 1, FAULT_PREFILL_K_TILE = 2 };
+enum : int { FAULT_NONE = 0, FAULT_DECODE_FINE_TILE = 1, FAULT_PREFILL_K_TILE = 2, FAULT_FULL_TILE = 3,
+             FAULT_FULL_BWD_TILE = 4 };
 #ifdef NSA_FAULT_INJECT
 #define NSA_INJECT(args, site) ((args).fault_site == (site))
 #else

@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
         const uint32_t ks = tiles & 1, vs = tiles % VS;
         if (tiles >= 2) ok = uwait(&bars->k_empty[ks], (tiles >> 1) - 1, 642);
         if (!ok) break;
-        if (lane == 0) {
+        if (lane == 0 && !(tiles == 0 && NSA_INJECT(a, FAULT_FULL_BWD_TILE))) {   // checking build: withhold the first
           mbar_arrive_expect_tx(&bars->k_full[ks], kKStage);
           for (int c = 0; c < KC; ++c)
             tma_load_3d(Qr + ks * kKStage + c * kPiece, &mp.q, &bars->k_full[ks], c * 64, sg.g * a.G, row);

@@ -304,6 +304,10 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
       // group: V of tile tv (none when < 0) and K of tile tk (none when >= n)
       auto push = [&](int tv, int tk) {
         uint64_t* bar = &bars->full[groups & 15];
+        if (groups == 0 && NSA_INJECT(a, FAULT_FULL_TILE)) {   // checking build: withhold the first tile
+          ++groups;
+          return;
+        }
         const bool v2 = tv >= 0 && (sg.kt0 + tv) * kFaKeys + 64 < sg.nkeys;   // the second 64 keys exist
         const bool k2 = tk < n && (sg.kt0 + tk) * kFaKeys + 64 < sg.nkeys;
         if (lane == 0)

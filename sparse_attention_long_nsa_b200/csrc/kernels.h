@@ -257,6 +257,7 @@ struct FullArgs {
   int H_q, H_kv, G, d_k, d_v;
   float scale_log2;       // softmax scale * log2(e)
   uint32_t* status;
+  int fault_site;         // checking build only: injected failure (FAULT_*), 0 = none
   // prompts: sequences sorted by length (longest first); tile_prefix[i] = query
   // blocks of the levels that sequences 0 .. i-1 end in (see PrefillSched)
   SeqTable seqs;
@@ -290,6 +291,7 @@ struct FullBwdArgs {
   int H_q, H_kv, G, batch;
   float scale, scale_log2;
   uint32_t* status;
+  int fault_site;         // checking build only: injected failure (FAULT_*), 0 = none
   int64_t n_rows;         // N * H_q
   int64_t n_items;        // row tiles x H_kv (query side)
   int64_t kv_prefix[kMaxBatch + 1];   // row tiles of all key blocks of the sequences before

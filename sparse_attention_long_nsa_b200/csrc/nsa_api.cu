@@ -24,6 +24,8 @@ nsa_status_t cuda_fail(cudaError_t e, const char* where) {
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// an array of `size`-byte elements (null counts as aligned)
+inline bool aligned_to(const void* p, size_t size) { return (reinterpret_cast<uintptr_t>(p) & (size - 1)) == 0; }
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 bool heads_supported(const nsa_heads_t* h) {
@@ -272,7 +274,7 @@ extern "C" {
 
 #ifdef NSA_FAULT_INJECT
 nsa_status_t nsa_test_set_fault(int32_t site) {
-  if (site < FAULT_NONE || site > FAULT_PREFILL_K_TILE) return NSA_ERR_INVALID_ARG;
+  if (site < FAULT_NONE || site > FAULT_FULL_BWD_TILE) return NSA_ERR_INVALID_ARG;
   nsa::g_test_fault = site;
   return NSA_OK;
 }
@@ -1101,6 +1103,7 @@ void fill_full_args(FullArgs& a, const nsa_heads_t* h, float scale, void* out, f
   a.H_q = h->H_q; a.H_kv = h->H_kv; a.G = h->H_q / h->H_kv; a.d_k = h->d_k; a.d_v = h->d_v;
   a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)h->d_k)) * 1.4426950408889634f;
   a.status = reinterpret_cast<uint32_t*>(ws);
+  a.fault_site = test_fault_site();
 }
 
 // the sequences sorted by length, longest first, with the blocks of `tok` tokens
@@ -1181,6 +1184,9 @@ nsa_status_t tree_common(const void* q, const void* k, const void* v, const int3
   if (!q || !k || !v || !cache_lens || !out || !workspace) return NSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(workspace))
     return NSA_ERR_INVALID_ARG;
+  if (!aligned_to(cache_lens, 4) || !aligned_to(n_nodes, 4) || !aligned_to(tree_mask, 8) || !aligned_to(lse_out, 4) ||
+      !aligned_to(pt.table, 4))
+    return NSA_ERR_INVALID_ARG;
   if (max_len <= 0 || Lmax < max_len || !(scale >= 0.f) || !(scale < INFINITY)) return NSA_ERR_INVALID_ARG;
   const int G = heads->H_q / heads->H_kv;
   const int nt = max_nodes * G > 128 ? 2 : 1, tok = nt * 128 / G;
@@ -1246,7 +1252,8 @@ nsa_status_t nsa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, in
       (v && !rows_ok(v, v_stride, (int64_t)heads->H_kv * heads->d_v)))
     return NSA_ERR_INVALID_ARG;
   if (!w_q || !w_k || !positions || !q_out || !k_out || (rope->d_rot > 0 && !inv_freq)) return NSA_ERR_INVALID_ARG;
-  if (!aligned16(w_q) || !aligned16(w_k) || !aligned16(q_out) || !aligned16(k_out) || (v_out && !aligned16(v_out)))
+  if (!aligned16(w_q) || !aligned16(w_k) || !aligned16(q_out) || !aligned16(k_out) || (v_out && !aligned16(v_out)) ||
+      !aligned_to(inv_freq, 4) || !aligned_to(positions, 4) || !aligned_to(cache_rows, 8))
     return NSA_ERR_INVALID_ARG;
   if (N > INT32_MAX) return NSA_ERR_UNSUPPORTED;
   if (N == 0) return NSA_OK;
@@ -1281,7 +1288,8 @@ nsa_status_t nsa_qk_norm_rope_backward(const void* q, int64_t q_stride, const vo
   if (!w_q || !w_k || !positions || !dq_out || !dk_out || !dw_q || !dw_k || !workspace ||
       (rope->d_rot > 0 && !inv_freq))
     return NSA_ERR_INVALID_ARG;
-  if (!aligned16(w_q) || !aligned16(w_k) || !aligned16(dq_out) || !aligned16(dk_out) || !aligned16(workspace))
+  if (!aligned16(w_q) || !aligned16(w_k) || !aligned16(dq_out) || !aligned16(dk_out) || !aligned16(workspace) ||
+      !aligned_to(inv_freq, 4) || !aligned_to(positions, 4) || !aligned_to(dw_q, 4) || !aligned_to(dw_k, 4))
     return NSA_ERR_INVALID_ARG;
   if (N > INT32_MAX) return NSA_ERR_UNSUPPORTED;
   if (ws_bytes < 256 + align256((size_t)kRopeBwdBlocks * 2 * heads->d_k * 4)) return NSA_ERR_WORKSPACE;
@@ -1318,6 +1326,7 @@ nsa_status_t nsa_full_prefill(const void* q, const void* k, const void* v, const
   if (!q || !k || !v || !cu_seqlens || !out || !workspace) return NSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(workspace))
     return NSA_ERR_INVALID_ARG;
+  if (!aligned_to(lse_out, 4)) return NSA_ERR_INVALID_ARG;
   if (cu_seqlens[0] != 0 || !(scale >= 0.f) || !(scale < INFINITY)) return NSA_ERR_INVALID_ARG;
   FullArgs a{};
   fill_full_args(a, heads, scale, out, lse_out, workspace);
@@ -1358,6 +1367,7 @@ nsa_status_t nsa_full_prefill_backward(const void* q, const void* k, const void*
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(dout) || !aligned16(dq) ||
       !aligned16(dk) || !aligned16(dv) || !aligned16(workspace))
     return NSA_ERR_INVALID_ARG;
+  if (!aligned_to(lse, 4)) return NSA_ERR_INVALID_ARG;
   if (cu_seqlens[0] != 0 || !(scale >= 0.f) || !(scale < INFINITY)) return NSA_ERR_INVALID_ARG;
   FullBwdArgs a{};
   a.H_q = heads->H_q; a.H_kv = heads->H_kv; a.G = heads->H_q / heads->H_kv; a.batch = batch;
@@ -1376,6 +1386,7 @@ nsa_status_t nsa_full_prefill_backward(const void* q, const void* k, const void*
   a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)heads->d_k);
   a.scale_log2 = a.scale * 1.4426950408889634f;
   a.status = reinterpret_cast<uint32_t*>(ws);
+  a.fault_site = test_fault_site();
   a.n_rows = N * heads->H_q;
   a.n_items = blocks * heads->H_kv;
   int64_t tiles = 0;

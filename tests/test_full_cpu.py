@@ -65,7 +65,7 @@ def rope_call(L, h=H, d_rot=64, inter=0, eps=1e-6, q=16, qs=None, k=16, ks=None,
 def test_rope_refusals(L):
     assert rope_call(L, N=0, n_rows=0) == nsa.NSA_OK                       # nothing to do: nothing is launched
     for kw in (dict(q=None), dict(q=8), dict(k=None), dict(k=24), dict(w=None), dict(w=8), dict(f=None), dict(pos=None),
-               dict(qo=None), dict(qo=8), dict(ko=None), dict(ko=20), dict(v=None), dict(vo=None), dict(v=8), dict(vo=8),
+               dict(f=18), dict(pos=17), dict(rows=20), dict(qo=None), dict(qo=8), dict(ko=None), dict(ko=20), dict(v=None), dict(vo=None), dict(v=8), dict(vo=8),
                dict(N=-1), dict(n_rows=9), dict(n_rows=-1, rows=16), dict(qs=64 * 192 - 8), dict(ks=4 * 192 + 4),
                dict(vs=4 * 128 - 8), dict(d_rot=-16), dict(d_rot=208), dict(eps=0.0), dict(eps=-1.0), dict(eps=float("nan")),
                dict(eps=float("inf")), dict(h=nsa.Heads(64, 3, 192, 128))):

@@ -245,3 +245,41 @@ def test_checking_build_agrees():
     with nsa.checking_library():
         got = run()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("what", ["prompt", "short prompt", "drafts", "gradient"])
+def test_withheld_tile_is_recorded_and_the_next_call_is_right(what):
+    """Checking build: a loader withholds a tile, the waits on it run out (20 ms), the
+    status word says so; the next call on the same workspace is right again."""
+    h = nsa.Heads(16, 2, 128, 128)
+    T = 70 if what == "short prompt" else 1500
+    q, k, v, cu = prompt([T], h, 80)
+    do = randn((T, 16, 128), gen(81))
+    out, lse = run_prefill(q, k, v, cu, h)
+    ws = nsa.alloc_workspace(max(nsa.nsa_full_workspace_size(nsa.NSA_OP_FULL_BACKWARD, h, 1, T, T, 0),
+                                 nsa.nsa_full_workspace_size(nsa.NSA_OP_TREE_DECODE, h, 1, 0, T, 4)), "cuda")
+    lens = torch.tensor([T], dtype=torch.int32, device="cuda")
+
+    def call():
+        o, l = torch.zeros_like(out), torch.zeros_like(lse)
+        g = [torch.zeros_like(t) for t in (q, k, v)]
+        if what == "gradient":
+            nsa.nsa_full_prefill_backward(q, k, v, out, lse, do, cu, h, *g, ws)
+        elif what == "drafts":
+            o = torch.zeros((1, 4, 16, 128), dtype=BF, device="cuda")
+            nsa.nsa_full_tree_decode(q[T - 4:].unsqueeze(0).contiguous(), k.unsqueeze(0), v.unsqueeze(0), lens, None, None, T, h, o,
+                                     None, ws)
+        else:
+            nsa.nsa_full_prefill(q, k, v, cu, h, o, l, ws)
+        nsa.nsa_check_device_status(ws)
+        return [o, l, *g]
+    want = call()
+    with nsa.checking_library():
+        nsa.nsa_test_set_fault(nsa.FAULT_FULL_BWD_TILE if what == "gradient" else nsa.FAULT_FULL_TILE)
+        try:
+            with pytest.raises(nsa.NSAError) as e:
+                call()
+            assert e.value.status == nsa.NSA_ERR_DEVICE_CHECK
+        finally:
+            nsa.nsa_test_set_fault(nsa.FAULT_NONE)
+        assert all(torch.equal(a, b) for a, b in zip(call(), want))
