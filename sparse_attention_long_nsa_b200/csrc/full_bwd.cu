@@ -18,8 +18,11 @@
 // S and dP are formed twice, seven products instead of five: one pass that also
 // accumulated dQ would add fp32 atomics in an order that differs between runs.
 //
-// Tensor memory (512 columns) of bwd_kv: S^T 128, over which P^T (64) is written;
-// dP^T 128 from column 64 on, over which dS^T (64) is written; dV 128, dK 192.
+// Tensor memory (512 columns) of bwd_kv: S^T 0-127, over whose first half P^T is
+// written; dP^T 64-191, over whose second half dS^T is written; dV 128, dK 192. That
+// leaves S^T of the next row tile free to be formed while dS^T of this one is: the
+// products run dP, dV, next S, dK, and each waits for work that the one or two before
+// it hid (without the look-ahead every tile waited for its whole chain).
 // bwd_q: S 128, dP 128, dQ 192, dS 64.
 #include "common.cuh"
 #include "kernels.h"
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
                                                                       const __grid_constant__ FullBwdMaps mp) {
   constexpr int KC = DK / 64, VC = DV / 64, VS = wide_stages(DK, DV);
   constexpr int kKStage = KC * kPiece, kVStage = VC * kPiece;
-  constexpr uint32_t kColDP = 64, kColDV = 192, kColDK = 320;
+  constexpr uint32_t kColDP = 64, kColDS = 128, kColDV = 192, kColDK = 320;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* Ks = smem;                       // K pieces, then V pieces
@@ -277,13 +280,14 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
       ok = uwait(&bars->fix_full, segs, 651);
       if (!ok) break;
       ++segs;
-#pragma unroll 1
-      for (int j = 0; j < n && ok; ++j, ++tiles) {
-        const uint32_t ks = tiles & 1, vs = tiles % VS;
+      // S^T of tile j = K Q^T: over P of the tile before (its dV is issued) and the half of
+      // its dP that has been read
+      auto scores = [&](int j, uint32_t t) {
+        const uint32_t ks = t & 1;
         const int left = min(L - (r0 + j) * TOK, TOK) * a.G;   // rows of the tile that exist
-        // S^T = K Q^T over the P and dS that the products before it have read
-        ok = uwait(&bars->k_full[ks], tiles >> 1, 652);
-        if (!ok) break;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_full[ks], (t >> 1) & 1, abort_flag, a.status, 652) &&
+                                         (j == 0 || mbar_wait(&bars->dp_read, (t - 1) & 1, abort_flag, a.status, 657)));
+        if (!ok) return;
         if (left < kRows) {
           for (int c = 0; c < KC; ++c) clear_rows(Qr + ks * kKStage + c * kPiece, left, lane);
           fence_proxy_async_smem();
@@ -299,37 +303,49 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
           }
           umma_commit(&bars->s_full);
         }
-        // dP^T = V dO^T beside P: the upper columns of S^T have to be read
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[vs], (tiles / VS) & 1, abort_flag, a.status, 653) &&
-                                         mbar_wait(&bars->s_read, tiles & 1, abort_flag, a.status, 654));
-        if (!ok) break;
-        if (left < kRows) {
-          for (int c = 0; c < VC; ++c) clear_rows(Gr + vs * kVStage + c * kPiece, left, lane);
-          fence_proxy_async_smem();
+        __syncwarp();
+      };
+      // step j: dP, dV of tile j, S of tile j + 1, dK of tile j (j = -1: S of tile 0)
+#pragma unroll 1
+      for (int j = -1; j < n && ok; ++j) {
+        const uint32_t ks = tiles & 1, vs = tiles % VS;   // of tile j
+        if (j >= 0) {
+          const int left = min(L - (r0 + j) * TOK, TOK) * a.G;
+          // dP^T = V dO^T beside P: the upper columns of S^T have to be read
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[vs], (tiles / VS) & 1, abort_flag, a.status, 653) &&
+                                           mbar_wait(&bars->s_read, tiles & 1, abort_flag, a.status, 654));
+          if (!ok) break;
+          if (left < kRows) {
+            for (int c = 0; c < VC; ++c) clear_rows(Gr + vs * kVStage + c * kPiece, left, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (elect_one()) {
+            tc_fence_after();
+            const uint64_t g = gs + (uint64_t)(vs * (kVStage >> 4));
+#pragma unroll
+            for (int kk = 0; kk < VC * 4; ++kk) {
+              const uint64_t o = (uint64_t)((kk >> 2) * (kPiece >> 4) + (kk & 3) * 2);
+              umma_ss(tm + kColDP, vd + o, g + o, id_s, kk ? 1u : 0u);
+            }
+            umma_commit(&bars->dp_full);
+            if (j + 1 == n) umma_commit(&bars->fix_empty);
+          }
+          // dV += P^T dO
+          ok = uwait(&bars->p_full, tiles, 655);
+          if (!ok) break;
+          if (elect_one()) {
+            tc_fence_after();
+            const uint64_t g = gt + (uint64_t)(vs * (kVStage >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              umma_ts(tm + kColDV, tm + kk * 8, g + (uint64_t)(kk * (2048 >> 4)), id_v, (j | kk) ? 1u : 0u);
+            umma_commit(&bars->v_empty[vs]);
+          }
           __syncwarp();
         }
-        if (elect_one()) {
-          tc_fence_after();
-          const uint64_t g = gs + (uint64_t)(vs * (kVStage >> 4));
-#pragma unroll
-          for (int kk = 0; kk < VC * 4; ++kk) {
-            const uint64_t o = (uint64_t)((kk >> 2) * (kPiece >> 4) + (kk & 3) * 2);
-            umma_ss(tm + kColDP, vd + o, g + o, id_s, kk ? 1u : 0u);
-          }
-          umma_commit(&bars->dp_full);
-          if (j + 1 == n) umma_commit(&bars->fix_empty);
-        }
-        // dV += P^T dO
-        ok = uwait(&bars->p_full, tiles, 655);
-        if (!ok) break;
-        if (elect_one()) {
-          tc_fence_after();
-          const uint64_t g = gt + (uint64_t)(vs * (kVStage >> 4));
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_ts(tm + kColDV, tm + kk * 8, g + (uint64_t)(kk * (2048 >> 4)), id_v, (j | kk) ? 1u : 0u);
-          umma_commit(&bars->v_empty[vs]);
-        }
+        if (j + 1 < n) scores(j + 1, j < 0 ? tiles : tiles + 1);
+        if (!ok || j < 0) continue;
         // dK += dS^T Q
         ok = uwait(&bars->ds_full, tiles, 656);
         if (!ok) break;
@@ -338,11 +354,12 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
           const uint64_t q = qt + (uint64_t)(ks * (kKStage >> 4));
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            umma_ts(tm + kColDK, tm + kColDP + kk * 8, q + (uint64_t)(kk * (2048 >> 4)), id_k, (j | kk) ? 1u : 0u);
+            umma_ts(tm + kColDK, tm + kColDS + kk * 8, q + (uint64_t)(kk * (2048 >> 4)), id_k, (j | kk) ? 1u : 0u);
           umma_commit(&bars->k_empty[ks]);
           if (j + 1 == n) umma_commit(&bars->acc_full);
         }
         __syncwarp();
+        ++tiles;
       }
     }
     if (elect_one()) {   // every product has finished before tensor memory is released
@@ -453,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
         ok = uwait(&bars->dp_read, tiles, 675);   // dS^T lies over columns that other warps read
         if (!ok) break;
         tc_fence_after();
-        tmem_st16(tmem + lane_base + kColDP + 16 * wq, w);
+        tmem_st16(tmem + lane_base + kColDS + 16 * wq, w);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&bars->ds_full);
