@@ -280,72 +280,75 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
       ok = uwait(&bars->fix_full, segs, 651);
       if (!ok) break;
       ++segs;
-      // S^T of tile j = K Q^T: over P of the tile before (its dV is issued) and the half of
-      // its dP that has been read
-      auto scores = [&](int j, uint32_t t) {
-        const uint32_t ks = t & 1;
-        const int left = min(L - (r0 + j) * TOK, TOK) * a.G;   // rows of the tile that exist
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_full[ks], (t >> 1) & 1, abort_flag, a.status, 652) &&
-                                         (j == 0 || mbar_wait(&bars->dp_read, (t - 1) & 1, abort_flag, a.status, 657)));
-        if (!ok) return;
+      // S^T of a tile = K Q^T at stage ks (one lane)
+      auto scores = [&](uint32_t ks) {
+        const uint64_t q = qs + (uint64_t)(ks * (kKStage >> 4));
+#pragma unroll
+        for (int kk = 0; kk < KC * 4; ++kk) {
+          const uint64_t o = (uint64_t)((kk >> 2) * (kPiece >> 4) + (kk & 3) * 2);
+          umma_ss(tm, kd + o, q + o, id_s, kk ? 1u : 0u);
+        }
+        umma_commit(&bars->s_full);
+      };
+      auto clear_q = [&](int j, uint32_t ks) {   // rows of tile j past the last token
+        const int left = min(L - (r0 + j) * TOK, TOK) * a.G;
         if (left < kRows) {
           for (int c = 0; c < KC; ++c) clear_rows(Qr + ks * kKStage + c * kPiece, left, lane);
           fence_proxy_async_smem();
           __syncwarp();
         }
-        if (elect_one()) {
-          tc_fence_after();
-          const uint64_t q = qs + (uint64_t)(ks * (kKStage >> 4));
-#pragma unroll
-          for (int kk = 0; kk < KC * 4; ++kk) {
-            const uint64_t o = (uint64_t)((kk >> 2) * (kPiece >> 4) + (kk & 3) * 2);
-            umma_ss(tm, kd + o, q + o, id_s, kk ? 1u : 0u);
-          }
-          umma_commit(&bars->s_full);
-        }
-        __syncwarp();
       };
-      // step j: dP, dV of tile j, S of tile j + 1, dK of tile j (j = -1: S of tile 0)
+      ok = uwait(&bars->k_full[tiles & 1], tiles >> 1, 652);
+      if (!ok) break;
+      clear_q(0, tiles & 1);
+      if (elect_one()) {
+        tc_fence_after();
+        scores(tiles & 1);
+      }
+      __syncwarp();
+      // step j: dP of tile j; dV of tile j and S of tile j + 1; dK of tile j
 #pragma unroll 1
-      for (int j = -1; j < n && ok; ++j) {
+      for (int j = 0; j < n && ok; ++j, ++tiles) {
         const uint32_t ks = tiles & 1, vs = tiles % VS;   // of tile j
-        if (j >= 0) {
-          const int left = min(L - (r0 + j) * TOK, TOK) * a.G;
-          // dP^T = V dO^T beside P: the upper columns of S^T have to be read
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[vs], (tiles / VS) & 1, abort_flag, a.status, 653) &&
-                                           mbar_wait(&bars->s_read, tiles & 1, abort_flag, a.status, 654));
-          if (!ok) break;
-          if (left < kRows) {
-            for (int c = 0; c < VC; ++c) clear_rows(Gr + vs * kVStage + c * kPiece, left, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (elect_one()) {
-            tc_fence_after();
-            const uint64_t g = gs + (uint64_t)(vs * (kVStage >> 4));
-#pragma unroll
-            for (int kk = 0; kk < VC * 4; ++kk) {
-              const uint64_t o = (uint64_t)((kk >> 2) * (kPiece >> 4) + (kk & 3) * 2);
-              umma_ss(tm + kColDP, vd + o, g + o, id_s, kk ? 1u : 0u);
-            }
-            umma_commit(&bars->dp_full);
-            if (j + 1 == n) umma_commit(&bars->fix_empty);
-          }
-          // dV += P^T dO
-          ok = uwait(&bars->p_full, tiles, 655);
-          if (!ok) break;
-          if (elect_one()) {
-            tc_fence_after();
-            const uint64_t g = gt + (uint64_t)(vs * (kVStage >> 4));
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_ts(tm + kColDV, tm + kk * 8, g + (uint64_t)(kk * (2048 >> 4)), id_v, (j | kk) ? 1u : 0u);
-            umma_commit(&bars->v_empty[vs]);
-          }
+        const int left = min(L - (r0 + j) * TOK, TOK) * a.G;
+        // dP^T = V dO^T beside P: the upper columns of S^T have to be read
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[vs], (tiles / VS) & 1, abort_flag, a.status, 653) &&
+                                         mbar_wait(&bars->s_read, tiles & 1, abort_flag, a.status, 654));
+        if (!ok) break;
+        if (left < kRows) {
+          for (int c = 0; c < VC; ++c) clear_rows(Gr + vs * kVStage + c * kPiece, left, lane);
+          fence_proxy_async_smem();
           __syncwarp();
         }
-        if (j + 1 < n) scores(j + 1, j < 0 ? tiles : tiles + 1);
-        if (!ok || j < 0) continue;
+        if (elect_one()) {
+          tc_fence_after();
+          const uint64_t g = gs + (uint64_t)(vs * (kVStage >> 4));
+#pragma unroll
+          for (int kk = 0; kk < VC * 4; ++kk) {
+            const uint64_t o = (uint64_t)((kk >> 2) * (kPiece >> 4) + (kk & 3) * 2);
+            umma_ss(tm + kColDP, vd + o, g + o, id_s, kk ? 1u : 0u);
+          }
+          umma_commit(&bars->dp_full);
+          if (j + 1 == n) umma_commit(&bars->fix_empty);
+        }
+        __syncwarp();
+        // dV += P^T dO; then S over P and the half of dP that has been read
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(&bars->p_full, tiles & 1, abort_flag, a.status, 655) &&
+                            (j + 1 == n || (mbar_wait(&bars->k_full[ks ^ 1], ((tiles + 1) >> 1) & 1, abort_flag, a.status, 652) &&
+                                            mbar_wait(&bars->dp_read, tiles & 1, abort_flag, a.status, 657))));
+        if (!ok) break;
+        if (j + 1 < n) clear_q(j + 1, ks ^ 1);
+        if (elect_one()) {
+          tc_fence_after();
+          const uint64_t g = gt + (uint64_t)(vs * (kVStage >> 4));
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts(tm + kColDV, tm + kk * 8, g + (uint64_t)(kk * (2048 >> 4)), id_v, (j | kk) ? 1u : 0u);
+          umma_commit(&bars->v_empty[vs]);
+          if (j + 1 < n) scores(ks ^ 1);
+        }
+        __syncwarp();
         // dK += dS^T Q
         ok = uwait(&bars->ds_full, tiles, 656);
         if (!ok) break;
@@ -359,7 +362,6 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_kv_kernel(const Full
           if (j + 1 == n) umma_commit(&bars->acc_full);
         }
         __syncwarp();
-        ++tiles;
       }
     }
     if (elect_one()) {   // every product has finished before tensor memory is released
@@ -687,9 +689,12 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_q_kernel(const FullB
         if (j < n) {
           const uint32_t ks = tiles & 1, vs = tiles % VS;
           const int left = keys - j * kRows;   // keys in sight
+          // all that S and dP of the tile need, in one round
           ok = __all_sync(0xffffffffu,
                           mbar_wait(&bars->k_full[ks], (tiles >> 1) & 1, abort_flag, a.status, 693) &&
-                              (tiles == 0 || mbar_wait(&bars->s_read, (tiles - 1) & 1, abort_flag, a.status, 692)));
+                              mbar_wait(&bars->v_full[vs], (tiles / VS) & 1, abort_flag, a.status, 695) &&
+                              (tiles == 0 || (mbar_wait(&bars->s_read, (tiles - 1) & 1, abort_flag, a.status, 692) &&
+                                              mbar_wait(&bars->dp_read, (tiles - 1) & 1, abort_flag, a.status, 694))));
           if (!ok) break;
           if (left < kRows) {   // dS is zero there, but 0 x NaN is not
             for (int c = 0; c < KC; ++c) clear_rows(Kr + ks * kKStage + c * kPiece, left, lane);
@@ -698,21 +703,13 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_q_kernel(const FullB
           }
           if (elect_one()) {
             tc_fence_after();
-            const uint64_t k = kd + (uint64_t)(ks * (kKStage >> 4));
+            const uint64_t k = kd + (uint64_t)(ks * (kKStage >> 4)), v = vd + (uint64_t)(vs * (kVStage >> 4));
 #pragma unroll
             for (int kk = 0; kk < KC * 4; ++kk) {
               const uint64_t o = (uint64_t)((kk >> 2) * (kPiece >> 4) + (kk & 3) * 2);
               umma_ss(tm, qd + o, k + o, id_s, kk ? 1u : 0u);
             }
             umma_commit(&bars->s_full);
-          }
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait(&bars->v_full[vs], (tiles / VS) & 1, abort_flag, a.status, 695) &&
-                              (tiles == 0 || mbar_wait(&bars->dp_read, (tiles - 1) & 1, abort_flag, a.status, 694)));
-          if (!ok) break;
-          if (elect_one()) {
-            tc_fence_after();
-            const uint64_t v = vd + (uint64_t)(vs * (kVStage >> 4));
 #pragma unroll
             for (int kk = 0; kk < VC * 4; ++kk) {
               const uint64_t o = (uint64_t)((kk >> 2) * (kPiece >> 4) + (kk & 3) * 2);
