@@ -269,9 +269,9 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
     uint32_t pos = 0;      // ring pieces issued
     uint32_t groups = 0;   // groups begun
     int q_n = 0;           // Q tiles issued
-    int blk, brow = 0;     // page table cache: lane i holds the row of 64-key block blk + i
+    int blk, brow = 0, blk2, brow2 = 0;   // page table windows: lane i holds the row of 64-key block blk + i
     while (ok && sched.next(sg)) {
-      blk = INT_MAX;       // another sequence: read anew
+      blk = blk2 = INT_MAX;   // another sequence: read anew
       if (q_n > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (q_n - 1) & 1, abort_flag, a.status, 611));
       if (!ok) break;
       const int n = max(sg.nt[0], sg.nt[1]);
@@ -286,17 +286,17 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
       }
       ++q_n;
       // rows of the two 64-key halves of key tile `t` (the second only if it has keys)
-      auto rows_of = [&](int t, int& r0, int& r1) {
+      auto rows_of = [&](int t, int& r0, int& r1, int& first, int& rows) {
         const int key = (sg.kt0 + t) * kFaKeys;
         if (TREE && a.pt.table) {
           const int kb = key >> 6;
-          if (kb < blk || kb - blk >= 32) {
-            blk = kb;
+          if (kb < first || kb - first >= 32) {
+            first = kb;
             const int e = (kb + lane) * 64;
-            brow = e < sg.nkeys ? (int)paged_row(a.pt, sg.b, e, a.status) : 0;
+            rows = e < sg.nkeys ? (int)paged_row(a.pt, sg.b, e, a.status) : 0;
           }
-          r0 = __shfl_sync(0xffffffffu, brow, kb - blk);
-          r1 = __shfl_sync(0xffffffffu, brow, (kb - blk + 1) & 31);   // kb - blk is even: never wraps
+          r0 = __shfl_sync(0xffffffffu, rows, kb - first);
+          r1 = __shfl_sync(0xffffffffu, rows, (kb - first + 1) & 31);   // kb - first is even: never wraps
         } else {
           r0 = (int)(sg.kv_row + key);
           r1 = r0 + 64;
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
         ++groups;
         int r0, r1;
         if (tv >= 0) {
-          rows_of(tv, r0, r1);
+          rows_of(tv, r0, r1, blk, brow);
 #pragma unroll
           for (int c = 0; c < VC; ++c) {
             uint8_t* dst = ring + acquire() * kFaSlot;
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
           }
         }
         if (tk < n) {
-          rows_of(tk, r0, r1);
+          rows_of(tk, r0, r1, blk, brow);
 #pragma unroll
           for (int c = 0; c < KC; ++c) {
             uint8_t* dst = ring + acquire() * kFaSlot;
@@ -352,9 +352,25 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
           }
         }
       };
+      // A cache comes from memory: beside 256 rows of Q the ring does not cover its latency,
+      // and the tile after the next is asked into L2 (16 nodes over 16K: 359 -> 339 us;
+      // with 128 rows the ring is deeper and it costs 1%, two tiles ahead cost 5%).
+      auto prefetch = [&](int t) {
+        int r0, r1;
+        rows_of(t, r0, r1, blk2, brow2);
+        if (lane < KC + VC) {
+          const CUtensorMap* m = lane < KC ? &mp.k : &mp.v;
+          const int c = (lane < KC ? lane : lane - KC) * 64;
+          tma_prefetch_3d(m, c, sg.g, r0);
+          if ((sg.kt0 + t) * kFaKeys + 64 < sg.nkeys) tma_prefetch_3d(m, c, sg.g, r1);
+        }
+        __syncwarp();
+      };
 #pragma unroll 1
-      for (int t = -A; t < n && ok; ++t)
+      for (int t = -A; t < n && ok; ++t) {
         if (t >= 0 || t + A < n) push(t < 0 ? -1 : t, t + A);
+        if (TREE && NT == 2 && t + A + 1 < n) prefetch(t + A + 1);
+      }
     }
     if (!ok && lane == 0) {   // let the copies still in flight land before the block exits
       if (q_n > 0) mbar_wait_drain(&bars->q_full, (q_n - 1) & 1);

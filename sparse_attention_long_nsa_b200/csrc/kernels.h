@@ -219,7 +219,7 @@ struct RopeArgs {
   int wpt;                // warps that share a token
   void *q_out, *k_out, *v_out;
 };
-constexpr int kRopeBwdBlocks = 296;   // two per SM
+constexpr int kRopeBwdBlocks = 148;   // one per SM
 struct RopeBwdArgs {
   RopeArgs f;             // q, k, weights, positions (nothing of the outputs)
   const void *dq_out, *dk_out;   // bf16 [N, H, d_k] gradients of the forward's outputs

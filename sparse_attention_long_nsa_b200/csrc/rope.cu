@@ -251,9 +251,11 @@ __global__ void __launch_bounds__(kThreads, 2) nsa_qk_norm_rope_kernel(const Rop
 
 // Backward. A thread sums the query weight's gradient of its channels in registers
 // and the key weight's (few heads) in shared memory of its own. part[block]: this
-// block's dw_q and dw_k, its lanes summed in a fixed order.
+// block's dw_q and dw_k, its lanes summed in a fixed order. At d_k = 192 a thread takes
+// 196 registers, one block an SM: held to two blocks it spilled, 177 us for 8K tokens
+// against 143.
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads, 2) nsa_qk_norm_rope_bwd_kernel(const RopeBwdArgs b) {
+__global__ void __launch_bounds__(kThreads, 1) nsa_qk_norm_rope_bwd_kernel(const RopeBwdArgs b) {
   constexpr int U = D / 64;
   extern __shared__ float4 sm_angles[];   // cosines and sines of each warp's token; at the end the warps' dw
   __shared__ float4 w_s[2][D / 4];
