@@ -464,7 +464,9 @@ nsa_status_t nsa_full_prefill(const void* q, const void* k, const void* v, const
  *   dq, dk, dv bf16 out [N, H_q, d_k], [N, H_kv, d_k], [N, H_kv, d_v], the types of
  *             the tensors they belong to; sums over keys, rows and the heads that
  *             share a key head are held in fp32 and rounded once
- * The same inputs give the same bits. N = 0 launches nothing. Workspace:
+ * The same inputs give the same bits. N = 0 launches nothing. As in the forward,
+ * NaN and infinity stay in their sequence; within it one may reach the gradients of
+ * tokens up to 255 away that the mask would spare. Workspace:
  * nsa_full_workspace_size(NSA_OP_FULL_BACKWARD, heads, batch, N, max_len, 0), which
  * serves nsa_full_prefill too. */
 nsa_status_t nsa_full_prefill_backward(const void* q, const void* k, const void* v, const void* out, const float* lse,

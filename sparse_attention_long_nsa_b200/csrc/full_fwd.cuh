@@ -32,6 +32,11 @@
 // (infinity or NaN) is not, so the issuing warp clears those rows in shared memory
 // first. Every wait is bounded; on a timeout the block stops, lets its copies and
 // products land and leaves.
+//
+// Measured: 8192 tokens, 64 heads on 4 key heads, 192 / 128: 1.12 ms by itself (1.22
+// PFLOP/s of 1.62 measured, tensor pipe 63 % active), 1.25 ms in a loop under the power
+// cap. 32 x 16 nodes over 16384 keys: 292 us (tensor pipe 51 %, 4.9 TB/s); 16 single
+// tokens over 8K to 128K keys: 515 us (5.8 TB/s).
 #pragma once
 
 #include <limits.h>

@@ -21,6 +21,8 @@
 // takes one token and four heads at a time: it forms the token's sines and cosines
 // (and, forward, their products with the weights) once, in registers, for all of its
 // heads; formed per head their loads and the index arithmetic bound the kernel.
+// 8192 tokens of 64 + 4 heads of 192: forward 90 us (4.7 TB/s of 6.55 measured),
+// backward 144 us (4.5 TB/s).
 #include "common.cuh"
 #include "kernels.h"
 
