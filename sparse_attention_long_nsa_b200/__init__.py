@@ -468,7 +468,7 @@ def _rows(t, n: int, heads: int, dim: int, dev: int, name: str) -> tuple:
     s0, s1, s2 = t.stride()
     if s2 != 1 or (heads > 1 and s1 != dim):
         raise ValueError(f"{name}: the heads of a token must be packed")
-    return t.data_ptr(), s0 if n > 1 else max(s0, heads * dim)
+    return t.data_ptr(), s0 if n > 1 else heads * dim   # one row: its stride means nothing
 
 
 _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64

@@ -175,6 +175,32 @@ def test_prefill(dims, Hq, Hk, lens):
     assert (out[N:] == 9).all() and (lse[N:] == 9).all()   # rows behind the last sequence
 
 
+@pytest.mark.parametrize("dims,Hq,Hk,lens", [((64, 64), 16, 16, [2600, 130, 1]), ((192, 128), 16, 16, [2433, 255]),
+                                             ((64, 128), 24, 12, [1700, 129]), ((128, 64), 40, 40, [1000])])
+def test_prefill_blocks_of_256_rows_whose_halves_end_in_different_tiles(dims, Hq, Hk, lens):
+    """One or two query heads a key head and enough blocks for all SMs: the second half
+    of a block sees a key tile that the first does not, or does not exist."""
+    h = nsa.Heads(Hq, Hk, *dims)
+    q, k, v, cu = prompt(lens, h, 5)
+    out, lse = run_prefill(q, k, v, cu, h)
+    want = R.prefill(q, k, v, lens, Hk, dims[0] ** -0.5)
+    R.assert_within(out, want["out"], want["out_tol"], "out")
+    R.assert_within(lse, want["lse"], want["lse_tol"], "lse")
+
+
+def test_prefill_largest_batch_and_many_empty_sequences():
+    h = nsa.Heads(8, 4, 64, 64)
+    lens = [(37 * i) % 90 if i % 3 else 0 for i in range(128)]
+    q, k, v, cu = prompt(lens, h, 6)
+    out, lse = run_prefill(q, k, v, cu, h)
+    do = randn(tuple(out.shape), gen(6))
+    want = R.prefill(q, k, v, lens, 4, 0.125, do)
+    R.assert_within(out, want["out"], want["out_tol"], "out")
+    R.assert_within(lse, want["lse"], want["lse_tol"], "lse")
+    for n, t in zip(("dq", "dk", "dv"), run_backward(q, k, v, cu, h, do)):
+        R.assert_within(t, want[n], want[n + "_tol"], n)
+
+
 def test_prefill_long_heads_of_the_8k_prompt():
     h = nsa.Heads(16, 1, 192, 128)
     q, k, v, cu = prompt([6000], h, 4)
@@ -407,6 +433,29 @@ def test_tree_chain_equals_mask_and_matches_prompt():
     r = R.prefill(q, k, v, [L], 4, 128 ** -0.5)
     R.assert_within(a[0][0], r["out"][L - M:], r["out_tol"][L - M:], "chain")
     R.assert_within(a[1][0], r["lse"][L - M:], r["lse_tol"][L - M:], "chain lse")
+
+
+@pytest.mark.parametrize("Lmax", [77, 129, 200])
+def test_tree_caches_of_odd_length(Lmax):
+    """Tiles reach into the next sequence's rows, which hold NaN, and past the cache."""
+    h = nsa.Heads(16, 4, 192, 64)
+    lens, nodes = [Lmax, 70, Lmax - 1, 1], [3, 2, 3, 1]
+    kv = caches(lens, Lmax, h, 44)
+    q = randn((4, 3, 16, 192), gen(3))
+    out, lse = run_tree(q, kv, lens, nodes, None, Lmax, h)
+    check_tree(out, lse, q, kv, lens, nodes, None, h, 192 ** -0.5)
+
+
+def test_tree_128_sequences():
+    h = nsa.Heads(4, 2, 64, 64)
+    lens = [1 + (53 * i) % 700 for i in range(128)]
+    nodes = [min(L, i % 5) for i, L in enumerate(lens)]
+    kv = caches(lens, 704, h, 45, page=64)
+    q = randn((128, 4, 4, 64), gen(4))
+    a = run_tree(q, kv, lens, nodes, None, 700, h)
+    check_tree(*a, q, kv, lens, nodes, None, h, 0.125)
+    b = run_tree(q, kv, lens, nodes, None, 700, h, paged=True)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 def test_tree_rows_that_see_nothing():
