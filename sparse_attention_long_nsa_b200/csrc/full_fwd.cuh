@@ -56,7 +56,9 @@ struct FaShape {
   static constexpr int kQBytes = NT * 128 * DK * 2;
   static constexpr int kMisc = 2048 + (NT == 1 ? 2048 : 0);
   static constexpr int kFit = (232448 - 1024 - kQBytes - kMisc) / kFaSlot;
-  static constexpr int kSlots = kFit > 12 ? 12 : kFit;
+  // a power of two for 256 rows (the slot of a piece is found by a mask: d = 128 205 -> 200
+  // us for ragged prompts); with 128 rows the deeper ring is worth more
+  static constexpr int kSlots = NT == 2 ? (kFit > 8 ? 8 : kFit) : kFit > 12 ? 12 : kFit;
   static constexpr int kSmem = 1024 + kQBytes + kSlots * kFaSlot + kMisc;
 };
 
