@@ -23,7 +23,7 @@
 // leaves S^T of the next row tile free to be formed while dS^T of this one is: the
 // products run dP, dV, next S, dK, and each waits for work that the one or two before
 // it hid (without the look-ahead every tile waited for its whole chain).
-// bwd_q: S 128, dP 128, dQ 192, dS 64; S and dP of the next tile are issued before dQ.
+// bwd_q: S 128, dP 128, dQ 192, dS 64; the next tile's S is issued before dQ.
 //
 // Measured, 4096 tokens, 64 heads on 4 key heads, 192 / 128: bwd_kv 657 us (four of the
 // seven products, 1.05 PFLOP/s, tensor pipe 57 % active), bwd_q 570 us (three, 0.96
@@ -672,76 +672,89 @@ __global__ void __launch_bounds__(kThreads, 1) nsa_full_bwd_q_kernel(const FullB
     if (!ok && lane == 0) drain_loads(bars, segs, k_n, v_n, VS);
   } else if (warp == 17) {
     // ------------------------------------------------------------ products
-    // S and dP of tile j + 1 are issued before dQ of tile j: both stages of K are in
-    // use then, V(j) is released by its dP
+    // S of tile j + 1 is issued before dQ of tile j: both stages of K are in use then
     const uint32_t tm = uni(tmem);
     const uint32_t id_s = umma_idesc_bf16(128, 128, false, false), id_k = umma_idesc_bf16(128, DK, false, true);
     const uint64_t qd = umma_desc_sw128(uni(smem_u32(Qs)), 16, 1024), gd = umma_desc_sw128(uni(smem_u32(Gs)), 16, 1024);
     const uint32_t k_a = uni(smem_u32(Kr)), v_a = uni(smem_u32(Vr));
     const uint64_t kd = umma_desc_sw128(k_a, 16, 1024), vd = umma_desc_sw128(v_a, 16, 1024);
     const uint64_t kt = umma_desc_sw128(k_a, kPiece, 1024);   // channels x keys
-    uint32_t tiles = 0;    // S issued
+    uint32_t tiles = 0;    // of the segments before
     int segs = 0;
     while (ok && next()) {
       const int n = uni(nkt), keys = uni(min(i0 + TOK, L));
       ok = uwait(&bars->fix_full, segs, 691);
       if (!ok) break;
       ++segs;
-      // step j: S and dP of tile j, then dQ of tile j - 1
-#pragma unroll 1
-      for (int j = 0; j <= n && ok; ++j) {
-        if (j < n) {
-          const uint32_t ks = tiles & 1, vs = tiles % VS;
-          const int left = keys - j * kRows;   // keys in sight
-          // all that S and dP of the tile need, in one round
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait(&bars->k_full[ks], (tiles >> 1) & 1, abort_flag, a.status, 693) &&
-                              mbar_wait(&bars->v_full[vs], (tiles / VS) & 1, abort_flag, a.status, 695) &&
-                              (tiles == 0 || (mbar_wait(&bars->s_read, (tiles - 1) & 1, abort_flag, a.status, 692) &&
-                                              mbar_wait(&bars->dp_read, (tiles - 1) & 1, abort_flag, a.status, 694))));
-          if (!ok) break;
-          if (left < kRows) {   // dS is zero there, but 0 x NaN is not
-            for (int c = 0; c < KC; ++c) clear_rows(Kr + ks * kKStage + c * kPiece, left, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (elect_one()) {
-            tc_fence_after();
-            const uint64_t k = kd + (uint64_t)(ks * (kKStage >> 4)), v = vd + (uint64_t)(vs * (kVStage >> 4));
-#pragma unroll
-            for (int kk = 0; kk < KC * 4; ++kk) {
-              const uint64_t o = (uint64_t)((kk >> 2) * (kPiece >> 4) + (kk & 3) * 2);
-              umma_ss(tm, qd + o, k + o, id_s, kk ? 1u : 0u);
-            }
-            umma_commit(&bars->s_full);
-#pragma unroll
-            for (int kk = 0; kk < VC * 4; ++kk) {
-              const uint64_t o = (uint64_t)((kk >> 2) * (kPiece >> 4) + (kk & 3) * 2);
-              umma_ss(tm + kColDP, gd + o, v + o, id_s, kk ? 1u : 0u);
-            }
-            umma_commit(&bars->v_empty[vs]);
-            umma_commit(&bars->dp_full);
-            if (j + 1 == n) umma_commit(&bars->fix_empty);
-          }
-          ++tiles;
+      auto scores = [&](int j) {   // S of tile j
+        const uint32_t t = tiles + j, ks = t & 1;
+        const int left = keys - j * kRows;   // keys in sight
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->k_full[ks], (t >> 1) & 1, abort_flag, a.status, 693) &&
+                                         (t == 0 || mbar_wait(&bars->s_read, (t - 1) & 1, abort_flag, a.status, 692)));
+        if (!ok) return;
+        if (left < kRows) {   // dS is zero there, but 0 x NaN is not
+          for (int c = 0; c < KC; ++c) clear_rows(Kr + ks * kKStage + c * kPiece, left, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
         }
-        if (j > 0) {
-          const uint32_t done = tiles - (j < n ? 2 : 1);   // number of tile j - 1
-          ok = uwait(&bars->ds_full, done, 696);
-          if (!ok) break;
-          if (elect_one()) {
-            tc_fence_after();
-            const uint64_t k = kt + (uint64_t)((done & 1) * (kKStage >> 4));
+        if (elect_one()) {
+          tc_fence_after();
+          const uint64_t k = kd + (uint64_t)(ks * (kKStage >> 4));
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_ts(tm + kColDQ, tm + kColDS + kk * 8, k + (uint64_t)(kk * (2048 >> 4)), id_k, (j > 1 || kk) ? 1u : 0u);
-            umma_commit(&bars->k_empty[done & 1]);
-            umma_commit(&bars->ds_free);
-            if (j == n) umma_commit(&bars->acc_full);
+          for (int kk = 0; kk < KC * 4; ++kk) {
+            const uint64_t o = (uint64_t)((kk >> 2) * (kPiece >> 4) + (kk & 3) * 2);
+            umma_ss(tm, qd + o, k + o, id_s, kk ? 1u : 0u);
           }
+          umma_commit(&bars->s_full);
         }
         __syncwarp();
+      };
+      auto weights = [&](int j) {   // dP of tile j
+        const uint32_t t = tiles + j, vs = t % VS;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->v_full[vs], (t / VS) & 1, abort_flag, a.status, 695) &&
+                                         (t == 0 || mbar_wait(&bars->dp_read, (t - 1) & 1, abort_flag, a.status, 694)));
+        if (!ok) return;
+        if (elect_one()) {
+          tc_fence_after();
+          const uint64_t v = vd + (uint64_t)(vs * (kVStage >> 4));
+#pragma unroll
+          for (int kk = 0; kk < VC * 4; ++kk) {
+            const uint64_t o = (uint64_t)((kk >> 2) * (kPiece >> 4) + (kk & 3) * 2);
+            umma_ss(tm + kColDP, gd + o, v + o, id_s, kk ? 1u : 0u);
+          }
+          umma_commit(&bars->v_empty[vs]);
+          umma_commit(&bars->dp_full);
+          if (j + 1 == n) umma_commit(&bars->fix_empty);
+        }
+        __syncwarp();
+      };
+      auto gradient = [&](int j) {   // dQ += dS K of tile j
+        const uint32_t t = tiles + j;
+        ok = uwait(&bars->ds_full, t, 696);
+        if (!ok) return;
+        if (elect_one()) {
+          tc_fence_after();
+          const uint64_t k = kt + (uint64_t)((t & 1) * (kKStage >> 4));
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_ts(tm + kColDQ, tm + kColDS + kk * 8, k + (uint64_t)(kk * (2048 >> 4)), id_k, (j | kk) ? 1u : 0u);
+          umma_commit(&bars->k_empty[t & 1]);
+          umma_commit(&bars->ds_free);
+          if (j + 1 == n) umma_commit(&bars->acc_full);
+        }
+        __syncwarp();
+      };
+      // S of a tile before dQ of the tile before. dP after that dQ where V has two stages
+      // (128 / 64: 19.5 us against 22 for the small training case), before it where it has
+      // one, so that its next tile is asked for early (192 / 128: 570 us against 599).
+#pragma unroll 1
+      for (int j = 0; j <= n && ok; ++j) {
+        if (j < n) scores(j);
+        if (VS == 1 && ok && j < n) weights(j);
+        if (ok && j > 0) gradient(j - 1);
+        if (VS > 1 && ok && j < n) weights(j);
       }
+      tiles += n;
     }
     if (elect_one()) {
       umma_commit(&bars->drain);
