@@ -344,6 +344,37 @@ def test_backward_same_bits_again_and_replayed():
     assert all(torch.equal(a, b) for a, b in zip(ref, g))
 
 
+def test_prompts_past_32_bit_offsets():
+    """128 sequences, 3.4e9 query elements: norm and rotation, attention and gradients of
+    the last sequence, which lies beyond 2^31 in every tensor but the keys'."""
+    h, L, B = nsa.Heads(64, 4, 192, 128), 2190, 128
+    lens = [L + 9 * (b == 5) for b in range(B)]
+    q, k, v, cu = prompt(lens, h, 23)
+    N = sum(lens)
+    assert N * 64 * 128 > 1 << 31
+    g = gen(24)
+    last = slice(N - L, N)
+    w = 1 + 0.1 * randn((192,), g, torch.float32)
+    f = torch.linspace(1, 1e-4, 48, device="cuda")
+    pos = torch.arange(N, device="cuda", dtype=torch.int32)
+    k_out = torch.empty_like(k)
+    nsa.nsa_qk_norm_rope(q, k, w, w, f, pos, h, nsa.RopeParams(96, 0, 1e-6), q, k_out)   # queries in place
+    x = prompt(lens, h, 23)[0][last]
+    want = R.rope(x, w, f, pos[last], 96, False, 1e-6)
+    big = (x.double().abs() * w.double()).amax(-1, keepdim=True) / torch.sqrt(x.double().square().mean(-1, keepdim=True))
+    R.assert_within(q[last], want, rope_tol(want, 2 * big), "rope")
+    del x, want, big
+    out, lse = run_prefill(q, k_out, v, cu, h)
+    do = randn((N, 64, 128), g)
+    dq, dk, dv = (torch.empty_like(t) for t in (q, k, v))
+    ws = ws_for(nsa.NSA_OP_FULL_BACKWARD, h, B, N, L + 9)
+    nsa.nsa_full_prefill_backward(q, k_out, v, out, lse, do, cu, h, dq, dk, dv, ws)
+    nsa.nsa_check_device_status(ws)
+    r = R.prefill(q[last], k_out[last], v[last], [L], 4, 192 ** -0.5, do[last])
+    for name, t in (("out", out), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        R.assert_within(t[last], r[name], r[name + "_tol"], name)
+
+
 # ---------------------------------------------------------------- drafted tokens over a cache
 
 def caches(lens, Lmax, h, seed, page=0, poison=True):
