@@ -492,7 +492,9 @@ nsa_status_t nsa_full_prefill_backward(const void* q, const void* k, const void*
  * Rows of nodes from n_nodes[b] on are left as they were (n_nodes[b] = 0: the
  * whole sequence). A node that sees nothing gets zeros and lse -infinity. Lengths
  * out of range are recorded in the status word and the sequence is skipped. Cache
- * rows from cache_lens[b] on are not read into a result. Workspace:
+ * rows from cache_lens[b] on, and those of nodes that no node's mask names (padded
+ * slots without n_nodes), are not read into a result. A value of a node that some
+ * nodes see, if it is not finite, may reach nodes of its sequence that do not. Workspace:
  * nsa_full_workspace_size(NSA_OP_TREE_DECODE, heads, batch, 0, max_len, max_nodes). */
 nsa_status_t nsa_full_tree_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* cache_lens,
                                   const int32_t* n_nodes, const uint64_t* tree_mask, int32_t batch,

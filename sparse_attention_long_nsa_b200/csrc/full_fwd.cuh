@@ -28,10 +28,11 @@
 // Q holds about one and a half tiles, and a common ring of small pieces keeps
 // more bytes in flight than separate rings of whole tiles would.
 //
-// The product of the tail's V rows past the last key: P is zero there, but 0 x
-// (infinity or NaN) is not, so the issuing warp clears those rows in shared memory
-// first. Every wait is bounded; on a timeout the block stops, lets its copies and
-// products land and leaves.
+// The product with V rows that no row of the block sees (past the last key; nodes that
+// no mask of the block's rows names): P is zero there, but 0 x (infinity or NaN) is not,
+// so the issuing warp clears those rows in shared memory first. A node that only some of
+// the rows see stays: a value of it that is not finite reaches the others too. Every wait
+// is bounded; on a timeout the block stops, lets its copies and products land and leaves.
 //
 // Measured: 8192 tokens, 64 heads on 4 key heads, 192 / 128: 1.12 ms by itself (1.22
 // PFLOP/s of 1.62 measured, tensor pipe 63 % active), 1.25 ms in a loop under the power
@@ -418,9 +419,21 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
     };
     while (ok && sched.next(sg)) {
       const int n0 = uni(sg.nt[0]), n1 = uni(sg.nt[1]), n = max(n0, n1), nkeys = uni(sg.nkeys), kt0 = uni(sg.kt0);
+      const int pre = uni(sg.prefix), seen_to = uni(sg.i0 + sg.ntok);   // nodes of the block's rows end there
+      uint64_t named = 0;   // tree: nodes that a row of the block sees (their words are read beside the tile's copies)
+      if (TREE && a.mask && (kt0 + n) * kFaKeys > pre)
+        for (int i = sg.i0 + lane; i < seen_to; i += 32) named |= a.mask[(int64_t)sg.b * a.M + i];
       ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full, segs & 1, abort_flag, a.status, 621));
       if (!ok) break;
       ++segs;
+      if (TREE) {
+        if (a.mask)
+          named = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(named >> 32)) << 32 |
+                  __reduce_or_sync(0xffffffffu, (uint32_t)named);
+        else
+          named = seen_to >= 64 ? ~0ull : (1ull << seen_to) - 1ull;
+        if (nkeys - pre < 64) named &= (1ull << (nkeys - pre)) - 1ull;
+      }
       // the first S of each buffer
 #pragma unroll 1
       for (int x = 0; x < 2 && ok; ++x) {
@@ -449,18 +462,26 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
                                            mbar_wait(&bars->p_full[x], (p_par >> x) & 1, abort_flag, a.status, 624));
           p_par ^= 1u << x;
           if (!ok) break;
-          const int left = nkeys - (kt0 + t) * kFaKeys;     // keys of this tile (may exceed 128)
-          if (left < kFaKeys && fresh) {                    // clear the V rows past the last key
+          const int key0 = (kt0 + t) * kFaKeys, left = nkeys - key0;   // keys of this tile (may exceed 128)
+          if (fresh && (TREE ? key0 + kFaKeys > pre : left < kFaKeys)) {   // clear the V rows no row sees
 #pragma unroll
-            for (int c = 0; c < VC; ++c) {
-              const int have = left - c * 64;
-              const int rows = VC == 1 && have > 64 ? 128 : 64;   // rows loaded
-              uint8_t* vs = ring + (p + c) % NS * kFaSlot;
-              if (have > 0 && have < rows)
-                for (int k = have * 8 + lane; k < rows * 8; k += 32) {
-                  *reinterpret_cast<uint4*>(vs + k * 16) = make_uint4(0, 0, 0, 0);
-                  if (VC == 2) *reinterpret_cast<uint4*>(vs + 8192 + k * 16) = make_uint4(0, 0, 0, 0);
-                }
+            for (int h = 0; h < 2; ++h) {                   // 64 keys each; bit i of `dead`: key 64 h + i
+              const int have = left - 64 * h;
+              if (have <= 0) continue;                      // not loaded
+              uint64_t dead;
+              if (TREE) {
+                const int j = key0 + 64 * h - pre;          // node of the first key
+                dead = j >= 64 ? ~0ull : j >= 0 ? ~(named >> j) : j > -64 ? ~named << -j : 0ull;
+              } else {
+                dead = have >= 64 ? 0ull : ~0ull << have;
+              }
+              if (dead == 0) continue;
+              uint8_t* vs = ring + (VC == 2 ? (p + h) % NS * kFaSlot : p % NS * kFaSlot + h * 8192);
+              for (int k = (__ffsll((long long)dead) - 1) * 8 + lane; k < 64 * 8; k += 32) {
+                if (!(dead >> (k >> 3) & 1)) continue;
+                *reinterpret_cast<uint4*>(vs + k * 16) = make_uint4(0, 0, 0, 0);
+                if (VC == 2) *reinterpret_cast<uint4*>(vs + 8192 + k * 16) = make_uint4(0, 0, 0, 0);
+              }
             }
             fence_proxy_async_smem();
             __syncwarp();

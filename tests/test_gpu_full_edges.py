@@ -1,0 +1,88 @@
+"""Full-attention operators on the GPU at the edges of their contracts, against the
+plain fp64 forms and bounds of tests/full_ref.py."""
+import pytest
+import torch
+
+import sparse_attention_long_nsa_b200 as nsa
+from tests import full_ref as R
+from tests.test_gpu_full import caches, check_tree, gen, randn, run_tree
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+# ---------------------------------------------------------------- nodes that no mask names
+
+def pages_of(k, v, page, seed):
+    """The rows of contiguous caches in shuffled pages: pools and block table."""
+    B, Lmax, per = k.shape[0], k.shape[1], k.shape[1] // page
+    perm = torch.randperm(B * per, generator=gen(seed), device="cuda")
+    pools = [torch.empty((B * per, page, *t.shape[2:]), dtype=BF, device="cuda") for t in (k, v)]
+    for p, t in zip(pools, (k, v)):
+        p[perm] = t.view(B * per, page, *t.shape[2:])
+    return (*pools, perm.to(torch.int32).view(B, per).contiguous())
+
+
+def tree_around(M, hidden, g):
+    """Words of a random tree over the nodes outside `hidden`; the others name nothing
+    and are named by nobody."""
+    words = [0] * M
+    live = [i for i in range(M) if i not in hidden]
+    for n, i in enumerate(live):
+        words[i] = 1 << i
+        if n:
+            words[i] |= words[live[int(torch.randint(0, n, (1,), generator=g))]]
+    return words
+
+
+@pytest.mark.parametrize("dims,Hq,Hk,M,lens,page", [
+    ((64, 64), 4, 1, 5, [5, 64, 130, 700], 0),          # 128 rows, V of 64 channels
+    ((192, 128), 16, 2, 8, [8, 150, 129, 1000], 64),    # 128 rows, V of 128 channels
+    ((128, 64), 16, 1, 16, [16, 70, 135, 2000], 64),    # 256 rows in one block
+    ((64, 128), 64, 4, 13, [13, 140, 6000], 0),         # 256 rows, the second half not full; cut units
+    ((128, 128), 32, 2, 64, [64, 150, 300, 1023], 128)])    # several blocks; nodes in two key tiles
+def test_tree_cache_rows_of_nodes_that_no_mask_names(dims, Hq, Hk, M, lens, page):
+    """Padded node slots without n_nodes: the slots' cache rows were never written and
+    hold NaN and infinities, no mask names them; every other node's result is as if they
+    were finite."""
+    h = nsa.Heads(Hq, Hk, *dims)
+    B, Lmax = len(lens), -(-max(lens) // 128) * 128
+    k, v = caches(lens, Lmax, h, 7 + M)[:2]
+    q = randn((B, M, Hq, dims[0]), gen(M))
+    cpu = torch.Generator().manual_seed(M)
+    masks = []
+    for b, L in enumerate(lens):
+        # padding at the end, nodes in the middle, the first node, all but the last
+        hidden = [set(range(M - M // 3 - 1, M)), {1, M // 2, M - 2}, {0, 2, M - 1}, set(range(M - 1))][b]
+        masks.append(tree_around(M, hidden, cpu))
+    good = run_tree(q, (k, v, None, None, None), lens, None, masks, max(lens), h)
+    for b, L in enumerate(lens):
+        for i in range(M):
+            if not any((w >> i) & 1 for w in masks[b]):
+                k[b, L - M + i] = float("nan") if i & 1 else float("-inf")
+                v[b, L - M + i] = float("inf") if i & 1 else float("nan")
+    kv = (k, v, *(pages_of(k, v, page, 5) if page else (None,) * 3))
+    out, lse = run_tree(q, kv, lens, None, masks, max(lens), h)
+    assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
+    check_tree(out, lse, q, kv, lens, [M] * B, masks, h, dims[0] ** -0.5)
+    if page:
+        po, pl = run_tree(q, kv, lens, None, masks, max(lens), h, paged=True)
+        assert torch.equal(po, out) and torch.equal(pl, lse)
+
+
+@pytest.mark.parametrize("dims", [(192, 128), (64, 64)])
+def test_tree_chain_longer_than_a_block_keeps_later_nodes_out(dims):
+    """33 drafts of 16 heads a group are three blocks of rows; the last draft's values
+    are NaN and reach its own rows only."""
+    h = nsa.Heads(16, 1, *dims)
+    lens, M = [500, 33], 33
+    k, v = caches(lens, 512, h, 8)[:2]
+    q = randn((2, M, 16, dims[0]), gen(9))
+    kv = (k, v, None, None, None)
+    good = run_tree(q, kv, lens, [M, M], None, 500, h)
+    for b, L in enumerate(lens):
+        v[b, L - 1] = float("nan")
+    out, lse = run_tree(q, kv, lens, [M, M], None, 500, h)
+    assert torch.equal(out[:, :M - 1], good[0][:, :M - 1]) and torch.equal(lse, good[1])
+    assert torch.isnan(out[:, M - 1].float()).all()
