@@ -233,7 +233,15 @@ __global__ void __launch_bounds__(kThreads, 2) nsa_qk_norm_rope_kernel(const Rop
             f[i] = v.x;
             f[i + 1] = v.y;
           }
-          mix_unit<INTER>(f, co[j]);
+          if (ch.rot) {
+            mix_unit<INTER>(f, co[j]);
+          } else {   // A and D only: 0 x (infinity or NaN) of the other channel is not 0
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              f[INTER ? 2 * i : i] *= co[j][0][i];
+              f[INTER ? 2 * i + 1 : 4 + i] *= co[j][3][i];
+            }
+          }
           uint2* dst = reinterpret_cast<uint2*>(y + (int64_t)h * D);
           dst[ch.c0] = pack4(f);
           dst[ch.c1] = pack4(f + 4);

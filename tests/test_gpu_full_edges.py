@@ -5,7 +5,7 @@ import torch
 
 import sparse_attention_long_nsa_b200 as nsa
 from tests import full_ref as R
-from tests.test_gpu_full import caches, check_tree, gen, randn, run_tree
+from tests.test_gpu_full import caches, check_tree, gen, randn, rope_tol, run_tree
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +86,29 @@ def test_tree_chain_longer_than_a_block_keeps_later_nodes_out(dims):
     out, lse = run_tree(q, kv, lens, [M, M], None, 500, h)
     assert torch.equal(out[:, :M - 1], good[0][:, :M - 1]) and torch.equal(lse, good[1])
     assert torch.isnan(out[:, M - 1].float()).all()
+
+
+# ---------------------------------------------------------------- norm and rotary position
+
+@pytest.mark.parametrize("d_k", [64, 192])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("d_rot", [0, 32])
+def test_rope_channels_that_do_not_rotate_stay_apart(d_k, inter, d_rot):
+    """A value or weight that is not finite, of a channel that does not rotate, is that
+    channel's alone (a value's norm apart)."""
+    h = nsa.Heads(4, 2, d_k, 64)
+    g = gen(3)
+    q, k = randn((9, 4, d_k), g), randn((9, 2, d_k), g)
+    w_q, w_k = (1 + 0.2 * randn((d_k,), g, torch.float32) for _ in range(2))
+    f = torch.linspace(1, 0.01, d_rot // 2, device="cuda")
+    pos = torch.arange(9, device="cuda", dtype=torch.int32) * 1000
+    for i, c in enumerate(range(d_rot, d_k, 5)):
+        q[i % 9, i % 4, c] = float("inf") if i & 1 else float("-inf")
+    w_q[d_rot + 1::7], w_k[d_rot + 2::9], w_k[d_k - 1] = float("inf"), float("-inf"), float("nan")
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    nsa.nsa_qk_norm_rope(q, k, w_q, w_k, f, pos, h, nsa.RopeParams(d_rot, int(inter), 1e-6), qo, ko)
+    for got, x, w in ((qo, q, w_q), (ko, k, w_k)):
+        want = R.rope(x, w, f, pos, d_rot, inter, 1e-6)
+        fin_w = torch.nan_to_num(w.double(), 0, 0, 0).abs()
+        big = (torch.nan_to_num(x.double(), 0, 0, 0).abs() * fin_w).amax(-1, keepdim=True) / torch.sqrt(x.double().square().mean(-1, keepdim=True) + 1e-6)
+        R.assert_within(got, want, rope_tol(want, 2 * big), "rope")
