@@ -423,7 +423,7 @@ typedef struct {
  *   q_out     bf16 out [N, H_q, d_k]; may be q when q is packed
  *   k_out     bf16 out [n_rows, H_kv, d_k]; may be k when packed and cache_rows is NULL
  *   v_out     bf16 out [n_rows, H_kv, d_v] or NULL
- * N = 0 launches nothing. No workspace. */
+ * N = 0 launches nothing, and the arrays of tokens and rows may be NULL. No workspace. */
 nsa_status_t nsa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                               int64_t v_stride, const float* w_q, const float* w_k, const float* inv_freq,
                               const int32_t* positions, const int64_t* cache_rows, int64_t n_rows, int64_t N,
@@ -434,7 +434,8 @@ nsa_status_t nsa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, in
  *   dq_out, dk_out  bf16 [N, H_q, d_k], [N, H_kv, d_k]: gradients of q_out, k_out
  *   dq, dk    bf16 out, token n at dq + n * dq_stride (dk_stride) elements:
  *             gradients of q, k
- *   dw_q, dw_k fp32 out [d_k]: summed over tokens and heads in a fixed order
+ *   dw_q, dw_k fp32 out [d_k]: summed over tokens and heads in a fixed order (zeros
+ *             for N = 0, where the arrays of tokens and the workspace may be NULL)
  * dq may be dq_out and dk may be dk_out (packed). Workspace:
  * nsa_full_workspace_size(NSA_OP_ROPE_BACKWARD, heads, 1, N, 0, 0). */
 nsa_status_t nsa_qk_norm_rope_backward(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
@@ -453,7 +454,8 @@ nsa_status_t nsa_qk_norm_rope_backward(const void* q, int64_t q_stride, const vo
  *             which nsa_full_prefill_backward takes
  * Rows past cu_seqlens[batch] are neither read into a result nor written; NaN or
  * infinity in one sequence does not reach another. Within a sequence a value that
- * is not finite may reach queries up to 127 tokens before it. Workspace:
+ * is not finite may reach queries up to 127 tokens before it. cu_seqlens[batch] = 0
+ * launches nothing, and the device arrays may be NULL. Workspace:
  * nsa_full_workspace_size(NSA_OP_FULL_PREFILL, heads, batch, N, max_len, 0). */
 nsa_status_t nsa_full_prefill(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, int32_t batch,
                               const nsa_heads_t* heads, float scale, void* out, float* lse_out, void* workspace,
@@ -464,9 +466,9 @@ nsa_status_t nsa_full_prefill(const void* q, const void* k, const void* v, const
  *   dq, dk, dv bf16 out [N, H_q, d_k], [N, H_kv, d_k], [N, H_kv, d_v], the types of
  *             the tensors they belong to; sums over keys, rows and the heads that
  *             share a key head are held in fp32 and rounded once
- * The same inputs give the same bits. N = 0 launches nothing. As in the forward,
- * NaN and infinity stay in their sequence; within it one may reach the gradients of
- * tokens up to 255 away that the mask would spare. Workspace:
+ * The same inputs give the same bits. N = 0 as in the forward. NaN and infinity stay
+ * in their sequence, too; within it one may reach the gradients of tokens up to 255
+ * away that the mask would spare. Workspace:
  * nsa_full_workspace_size(NSA_OP_FULL_BACKWARD, heads, batch, N, max_len, 0), which
  * serves nsa_full_prefill too. */
 nsa_status_t nsa_full_prefill_backward(const void* q, const void* k, const void* v, const void* out, const float* lse,

@@ -1167,10 +1167,10 @@ nsa_status_t check_rope(const nsa_heads_t* heads, const nsa_rope_params_t* rope)
   return rope->d_rot % 16 == 0 ? NSA_OK : NSA_ERR_UNSUPPORTED;
 }
 
-// rows of `width` packed elements at a stride: aligned, not overlapping
-bool rows_ok(const void* p, int64_t stride, int64_t width) {
-  return p && aligned16(p) && stride >= width && stride % 8 == 0;
-}
+// rows of `width` packed elements at a stride: not overlapping, aligned within the array
+bool stride_ok(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0; }
+// an array that is read or written in 16-byte units
+bool array_ok(const void* p) { return p && aligned16(p); }
 
 nsa_status_t tree_common(const void* q, const void* k, const void* v, const int32_t* cache_lens,
                          const int32_t* n_nodes, const uint64_t* tree_mask, int32_t batch, int32_t max_nodes,
@@ -1246,17 +1246,17 @@ nsa_status_t nsa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, in
   nsa_status_t s = check_rope(heads, rope);
   if (s != NSA_OK) return s;
   if (N < 0 || n_rows < 0 || (!cache_rows && n_rows < N)) return NSA_ERR_INVALID_ARG;
-  if ((v == nullptr) != (v_out == nullptr)) return NSA_ERR_INVALID_ARG;
-  if (!rows_ok(q, q_stride, (int64_t)heads->H_q * heads->d_k) ||
-      !rows_ok(k, k_stride, (int64_t)heads->H_kv * heads->d_k) ||
-      (v && !rows_ok(v, v_stride, (int64_t)heads->H_kv * heads->d_v)))
+  if (!stride_ok(q_stride, (int64_t)heads->H_q * heads->d_k) || !stride_ok(k_stride, (int64_t)heads->H_kv * heads->d_k) ||
+      (v && !stride_ok(v_stride, (int64_t)heads->H_kv * heads->d_v)))
     return NSA_ERR_INVALID_ARG;
-  if (!w_q || !w_k || !positions || !q_out || !k_out || (rope->d_rot > 0 && !inv_freq)) return NSA_ERR_INVALID_ARG;
-  if (!aligned16(w_q) || !aligned16(w_k) || !aligned16(q_out) || !aligned16(k_out) || (v_out && !aligned16(v_out)) ||
-      !aligned_to(inv_freq, 4) || !aligned_to(positions, 4) || !aligned_to(cache_rows, 8))
+  if (!array_ok(w_q) || !array_ok(w_k) || (rope->d_rot > 0 && !inv_freq) || !aligned_to(inv_freq, 4))
     return NSA_ERR_INVALID_ARG;
   if (N > INT32_MAX) return NSA_ERR_UNSUPPORTED;
-  if (N == 0) return NSA_OK;
+  if (N == 0) return NSA_OK;   // arrays without tokens may have no address
+  if ((v == nullptr) != (v_out == nullptr)) return NSA_ERR_INVALID_ARG;
+  if (!array_ok(q) || !array_ok(k) || !positions || !array_ok(q_out) || !array_ok(k_out) || !aligned16(v) ||
+      !aligned16(v_out) || !aligned_to(positions, 4) || !aligned_to(cache_rows, 8))
+    return NSA_ERR_INVALID_ARG;
   RopeArgs a{};
   a.q = q; a.k = k; a.v = v;
   a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
@@ -1282,23 +1282,22 @@ nsa_status_t nsa_qk_norm_rope_backward(const void* q, int64_t q_stride, const vo
   if (s != NSA_OK) return s;
   if (N < 0) return NSA_ERR_INVALID_ARG;
   const int64_t wq = (int64_t)heads->H_q * heads->d_k, wk = (int64_t)heads->H_kv * heads->d_k;
-  if (!rows_ok(q, q_stride, wq) || !rows_ok(k, k_stride, wk) || !rows_ok(dq, dq_stride, wq) ||
-      !rows_ok(dk, dk_stride, wk))
+  if (!stride_ok(q_stride, wq) || !stride_ok(k_stride, wk) || !stride_ok(dq_stride, wq) || !stride_ok(dk_stride, wk))
     return NSA_ERR_INVALID_ARG;
-  if (!w_q || !w_k || !positions || !dq_out || !dk_out || !dw_q || !dw_k || !workspace ||
-      (rope->d_rot > 0 && !inv_freq))
-    return NSA_ERR_INVALID_ARG;
-  if (!aligned16(w_q) || !aligned16(w_k) || !aligned16(dq_out) || !aligned16(dk_out) || !aligned16(workspace) ||
-      !aligned_to(inv_freq, 4) || !aligned_to(positions, 4) || !aligned_to(dw_q, 4) || !aligned_to(dw_k, 4))
+  if (!array_ok(w_q) || !array_ok(w_k) || !dw_q || !dw_k || (rope->d_rot > 0 && !inv_freq) || !aligned_to(inv_freq, 4) ||
+      !aligned_to(dw_q, 4) || !aligned_to(dw_k, 4))
     return NSA_ERR_INVALID_ARG;
   if (N > INT32_MAX) return NSA_ERR_UNSUPPORTED;
-  if (ws_bytes < 256 + align256((size_t)kRopeBwdBlocks * 2 * heads->d_k * 4)) return NSA_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (N == 0) {   // the sums over no tokens
+  if (N == 0) {   // the sums over no tokens; arrays without tokens may have no address
     cudaError_t e = cudaMemsetAsync(dw_q, 0, (size_t)heads->d_k * 4, st);
     if (e == cudaSuccess) e = cudaMemsetAsync(dw_k, 0, (size_t)heads->d_k * 4, st);
     return e == cudaSuccess ? NSA_OK : cuda_fail(e, "norm backward memset");
   }
+  if (!array_ok(q) || !array_ok(k) || !positions || !array_ok(dq_out) || !array_ok(dk_out) || !array_ok(dq) ||
+      !array_ok(dk) || !array_ok(workspace) || !aligned_to(positions, 4))
+    return NSA_ERR_INVALID_ARG;
+  if (ws_bytes < 256 + align256((size_t)kRopeBwdBlocks * 2 * heads->d_k * 4)) return NSA_ERR_WORKSPACE;
   RopeBwdArgs b{};
   RopeArgs& a = b.f;
   a.q = q; a.k = k;
@@ -1323,25 +1322,23 @@ nsa_status_t nsa_full_prefill(const void* q, const void* k, const void* v, const
   nsa_status_t s = check_heads(heads);
   if (s != NSA_OK) return s;
   if (batch <= 0 || batch > NSA_MAX_BATCH) return batch <= 0 ? NSA_ERR_INVALID_ARG : NSA_ERR_UNSUPPORTED;
-  if (!q || !k || !v || !cu_seqlens || !out || !workspace) return NSA_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(workspace))
-    return NSA_ERR_INVALID_ARG;
-  if (!aligned_to(lse_out, 4)) return NSA_ERR_INVALID_ARG;
-  if (cu_seqlens[0] != 0 || !(scale >= 0.f) || !(scale < INFINITY)) return NSA_ERR_INVALID_ARG;
+  if (!cu_seqlens || cu_seqlens[0] != 0 || !(scale >= 0.f) || !(scale < INFINITY)) return NSA_ERR_INVALID_ARG;
   FullArgs a{};
   fill_full_args(a, heads, scale, out, lse_out, workspace);
   // 256 rows a block when that gives every SM one, else 128 rows
   int nt = 2;
   int64_t blocks = fill_levels(a.seqs, cu_seqlens, batch, nt * 128 / a.G);
   if (blocks < 0) return NSA_ERR_INVALID_ARG;
+  const int64_t N = cu_seqlens[batch];
+  if (N == 0) return NSA_OK;   // arrays without tokens may have no address
+  if (!array_ok(q) || !array_ok(k) || !array_ok(v) || !array_ok(out) || !array_ok(workspace) || !aligned_to(lse_out, 4))
+    return NSA_ERR_INVALID_ARG;
   if (ws_bytes < 256) return NSA_ERR_WORKSPACE;
   if (blocks * a.H_kv < kFullBlocks) {
     nt = 1;
     blocks = fill_levels(a.seqs, cu_seqlens, batch, nt * 128 / a.G);
   }
   a.n_items = blocks * a.H_kv;
-  const int64_t N = cu_seqlens[batch];
-  if (N == 0) return NSA_OK;
   FullMaps m;
   memset(&m, 0, sizeof(m));
   if (!make_full_maps(m, q, N, k, v, N, heads)) {
@@ -1362,22 +1359,19 @@ nsa_status_t nsa_full_prefill_backward(const void* q, const void* k, const void*
   nsa_status_t s = check_heads(heads);
   if (s != NSA_OK) return s;
   if (batch <= 0 || batch > NSA_MAX_BATCH) return batch <= 0 ? NSA_ERR_INVALID_ARG : NSA_ERR_UNSUPPORTED;
-  if (!q || !k || !v || !out || !lse || !dout || !cu_seqlens || !dq || !dk || !dv || !workspace)
-    return NSA_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(dout) || !aligned16(dq) ||
-      !aligned16(dk) || !aligned16(dv) || !aligned16(workspace))
-    return NSA_ERR_INVALID_ARG;
-  if (!aligned_to(lse, 4)) return NSA_ERR_INVALID_ARG;
-  if (cu_seqlens[0] != 0 || !(scale >= 0.f) || !(scale < INFINITY)) return NSA_ERR_INVALID_ARG;
+  if (!cu_seqlens || cu_seqlens[0] != 0 || !(scale >= 0.f) || !(scale < INFINITY)) return NSA_ERR_INVALID_ARG;
   FullBwdArgs a{};
   a.H_q = heads->H_q; a.H_kv = heads->H_kv; a.G = heads->H_q / heads->H_kv; a.batch = batch;
   const int tok = 128 / a.G;
   const int64_t blocks = fill_levels(a.seqs, cu_seqlens, batch, tok);
   if (blocks < 0) return NSA_ERR_INVALID_ARG;
   const int64_t N = cu_seqlens[batch];
+  if (N == 0) return NSA_OK;   // arrays without tokens may have no address
+  if (!array_ok(q) || !array_ok(k) || !array_ok(v) || !array_ok(out) || !array_ok(dout) || !array_ok(dq) || !array_ok(dk) ||
+      !array_ok(dv) || !array_ok(workspace) || !lse || !aligned_to(lse, 4))
+    return NSA_ERR_INVALID_ARG;
   const FullBwdWs w = full_bwd_ws(heads, N);
   if (ws_bytes < w.total) return NSA_ERR_WORKSPACE;
-  if (N == 0) return NSA_OK;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.out = out; a.dout = dout; a.lse = lse; a.dq = dq; a.dk = dk; a.dv = dv;
   a.row = (float2*)(ws + w.row);

@@ -1,0 +1,54 @@
+"""Full-attention entry points at the edges of their contracts, without a GPU."""
+import ctypes
+import os
+
+import pytest
+
+import sparse_attention_long_nsa_b200 as nsa
+
+H = nsa.Heads(64, 4, 192, 128)
+INV, WS = nsa.NSA_ERR_INVALID_ARG, nsa.NSA_ERR_WORKSPACE
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(nsa.LIB_PATH):
+        from sparse_attention_long_nsa_b200 import build
+        build.build()
+    return nsa.lib()
+
+
+def ref(x):
+    return ctypes.byref(x)
+
+
+# ---------------------------------------------------------------- nothing to do
+
+def norm_call(L, N, q=None, v=None, v_out=None, w=16, n_rows=0, rows=None, d_rot=64, stride=64 * 192, k_out=None):
+    rp = nsa.RopeParams(d_rot, 0, 1e-6)
+    return L.nsa_qk_norm_rope(q, stride, q, 4 * 192, v, 4 * 128, w, w, 16, q, rows, n_rows, N, ref(H), ref(rp), q, k_out, v_out,
+                              None)
+
+
+def test_norm_of_no_tokens_takes_null_arrays(L):
+    """An empty array has no address: N = 0 is nothing to do, whatever the per-token
+    pointers are; geometry, weights and parameters are still checked."""
+    assert norm_call(L, 0) == nsa.NSA_OK
+    assert norm_call(L, 0, v_out=16, k_out=16, n_rows=5) == nsa.NSA_OK    # no values, a real cache
+    for kw in (dict(w=None), dict(w=8), dict(d_rot=-16), dict(n_rows=-1, rows=16), dict(stride=64 * 192 - 8)):
+        assert norm_call(L, 0, **kw) == INV, kw
+    assert norm_call(L, 1) == INV
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_attention_over_empty_prompts_takes_null_arrays(L, back):
+    def call(cu, scale=0.0, h=H):
+        arr = (ctypes.c_int32 * len(cu))(*cu)
+        if back:
+            return L.nsa_full_prefill_backward(None, None, None, None, None, None, arr, len(cu) - 1, ref(h), scale, None, None, None,
+                                               None, 0, None)
+        return L.nsa_full_prefill(None, None, None, arr, len(cu) - 1, ref(h), scale, None, None, None, 0, None)
+    assert call((0, 0)) == nsa.NSA_OK and call((0,) * 129) == nsa.NSA_OK
+    for cu in ((0, 5, 0), (1, 1), (0, -1), (0, -4, 0), (0, 0, 3)):
+        assert call(cu) == INV, cu
+    assert call((0, 0), scale=-1.0) == INV and call((0, 0), h=nsa.Heads(64, 3, 192, 128)) == INV
