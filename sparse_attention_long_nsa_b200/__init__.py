@@ -497,8 +497,11 @@ def _launch(dev: int, where: str, fn, *args):
         _check(s, where)
 
 
-def _ws(ws, dev: int):
+def _ws(ws, dev: int, n: int = 1):
+    """(pointer, bytes) of a workspace; a call of no tokens (n <= 0) needs none."""
     if ws is None:
+        if n <= 0:
+            return None, 0
         raise ValueError("ws: a workspace is needed (alloc_workspace of nsa_full_workspace_size bytes)")
     if ws.get_device() != dev or not ws.is_contiguous():
         _bad(ws, ws.dtype, dev, "ws")
@@ -538,8 +541,7 @@ def nsa_qk_norm_rope(q, k, w_q, w_k, inv_freq, positions, heads: Heads, rope: Ro
             None if cache_rows is None else _in(cache_rows, _I64, dev, (N,), "cache_rows"), n_rows, N,
             ctypes.byref(heads), ctypes.byref(rope), _in(q_out, _BF16, dev, (N, Hq, dk), "q_out"),
             _in(k_out, _BF16, dev, k_out.shape, "k_out"), vo, _raw_stream(dev, stream))
-    if N > 0:   # empty tensors have no address
-        _launch(dev, "nsa_qk_norm_rope", lib().nsa_qk_norm_rope, *args)
+    _launch(dev, "nsa_qk_norm_rope", lib().nsa_qk_norm_rope, *args)
 
 
 def nsa_qk_norm_rope_backward(q, k, w_q, w_k, inv_freq, positions, dq_out, dk_out, heads: Heads, rope: RopeParams, dq,
@@ -553,18 +555,13 @@ def nsa_qk_norm_rope_backward(q, k, w_q, w_k, inv_freq, positions, dq_out, dk_ou
     kp, ks = _rows(k, N, Hk, d, dev, "k")
     gqp, gqs = _rows(dq, N, Hq, d, dev, "dq")
     gkp, gks = _rows(dk, N, Hk, d, dev, "dk")
-    st = _raw_stream(dev, stream)
     args = (qp, qs, kp, ks, _in(w_q, _F32, dev, (d,), "w_q"), _in(w_k, _F32, dev, (d,), "w_k"),
             _in(inv_freq, _F32, dev, (dr // 2,), "inv_freq") if dr > 0 else None,
             _in(positions, _I32, dev, (N,), "positions"), N, _in(dq_out, _BF16, dev, (N, Hq, d), "dq_out"),
             _in(dk_out, _BF16, dev, (N, Hk, d), "dk_out"), ctypes.byref(heads), ctypes.byref(rope), gqp, gqs, gkp,
-            gks, _in(dw_q, _F32, dev, (d,), "dw_q"), _in(dw_k, _F32, dev, (d,), "dw_k"), *_ws(ws, dev), st)
-    if N > 0:
-        _launch(dev, "nsa_qk_norm_rope_backward", lib().nsa_qk_norm_rope_backward, *args)
-    else:       # empty tensors have no address; the sums over no tokens
-        with torch.cuda.stream(torch.cuda.ExternalStream(st, device=q.device)):
-            dw_q.zero_()
-            dw_k.zero_()
+            gks, _in(dw_q, _F32, dev, (d,), "dw_q"), _in(dw_k, _F32, dev, (d,), "dw_k"), *_ws(ws, dev, N),
+            _raw_stream(dev, stream))
+    _launch(dev, "nsa_qk_norm_rope_backward", lib().nsa_qk_norm_rope_backward, *args)
 
 
 def _batch_of(cu_seqlens) -> tuple:
@@ -584,12 +581,10 @@ def nsa_full_prefill(q, k, v, cu_seqlens, heads: Heads, out, lse_out=None, ws=No
     Hq, Hk, dk, dv = heads.H_q, heads.H_kv, heads.d_k, heads.d_v
     cu, B, N = _batch_of(cu_seqlens)
     dev = _device_of(q, "q")
-    if N == 0:   # empty tensors have no address
-        return
     _launch(dev, "nsa_full_prefill", lib().nsa_full_prefill, _in_rows(q, _BF16, dev, N, (Hq, dk), "q"),
             _in_rows(k, _BF16, dev, N, (Hk, dk), "k"), _in_rows(v, _BF16, dev, N, (Hk, dv), "v"), cu, B,
             ctypes.byref(heads), scale, _in_rows(out, _BF16, dev, N, (Hq, dv), "out"),
-            None if lse_out is None else _in_rows(lse_out, _F32, dev, N, (Hq,), "lse_out"), *_ws(ws, dev),
+            None if lse_out is None else _in_rows(lse_out, _F32, dev, N, (Hq,), "lse_out"), *_ws(ws, dev, N),
             _raw_stream(dev, stream))
 
 
@@ -600,14 +595,12 @@ def nsa_full_prefill_backward(q, k, v, out, lse, dout, cu_seqlens, heads: Heads,
     Hq, Hk, d, e = heads.H_q, heads.H_kv, heads.d_k, heads.d_v
     cu, B, N = _batch_of(cu_seqlens)
     dev = _device_of(q, "q")
-    if N == 0:
-        return
     _launch(dev, "nsa_full_prefill_backward", lib().nsa_full_prefill_backward,
             _in_rows(q, _BF16, dev, N, (Hq, d), "q"), _in_rows(k, _BF16, dev, N, (Hk, d), "k"),
             _in_rows(v, _BF16, dev, N, (Hk, e), "v"), _in_rows(out, _BF16, dev, N, (Hq, e), "out"),
             _in_rows(lse, _F32, dev, N, (Hq,), "lse"), _in_rows(dout, _BF16, dev, N, (Hq, e), "dout"), cu, B,
             ctypes.byref(heads), scale, _in_rows(dq, _BF16, dev, N, (Hq, d), "dq"),
-            _in_rows(dk, _BF16, dev, N, (Hk, d), "dk"), _in_rows(dv, _BF16, dev, N, (Hk, e), "dv"), *_ws(ws, dev),
+            _in_rows(dk, _BF16, dev, N, (Hk, d), "dk"), _in_rows(dv, _BF16, dev, N, (Hk, e), "dv"), *_ws(ws, dev, N),
             _raw_stream(dev, stream))
 
 

@@ -5,7 +5,7 @@ import torch
 
 import sparse_attention_long_nsa_b200 as nsa
 from tests import full_ref as R
-from tests.test_gpu_full import caches, check_tree, gen, randn, rope_tol, run_tree
+from tests.test_gpu_full import caches, check_tree, gen, randn, rope_tol, run_tree, ws_for
 
 pytestmark = pytest.mark.gpu
 
@@ -112,3 +112,40 @@ def test_rope_channels_that_do_not_rotate_stay_apart(d_k, inter, d_rot):
         fin_w = torch.nan_to_num(w.double(), 0, 0, 0).abs()
         big = (torch.nan_to_num(x.double(), 0, 0, 0).abs() * fin_w).amax(-1, keepdim=True) / torch.sqrt(x.double().square().mean(-1, keepdim=True) + 1e-6)
         R.assert_within(got, want, rope_tol(want, 2 * big), "rope")
+
+
+# ---------------------------------------------------------------- refusals of the binding
+
+def empty(*s):
+    return torch.empty(s, dtype=BF, device="cuda")
+
+
+@pytest.mark.parametrize("cu", [[0, 5, 0], [0, -4, 0], [1, 0], [0, -1]])
+def test_binding_leaves_bad_cu_seqlens_to_the_library(cu):
+    """A last entry of 0 does not make the others right."""
+    h = nsa.Heads(8, 2, 64, 64)
+    q, kv, lse = empty(0, 8, 64), empty(0, 2, 64), torch.empty((0, 8), device="cuda")
+    cu = torch.tensor(cu, dtype=torch.int32)
+    ws = ws_for(nsa.NSA_OP_FULL_BACKWARD, h, 2, 0, 0)
+    for call in (lambda: nsa.nsa_full_prefill(q, kv, kv, cu, h, q, lse, ws),
+                 lambda: nsa.nsa_full_prefill(q, kv, kv, cu, h, q),
+                 lambda: nsa.nsa_full_prefill_backward(q, kv, kv, q, lse, q, cu, h, q, kv, kv, ws)):
+        with pytest.raises(nsa.NSAError) as e:
+            call()
+        assert e.value.status == nsa.NSA_ERR_INVALID_ARG
+
+
+def test_empty_calls_need_no_workspace():
+    h, rp = nsa.Heads(8, 2, 64, 64), nsa.RopeParams(0, 0, 1e-6)
+    q, kv, lse = empty(0, 8, 64), empty(0, 2, 64), torch.empty((0, 8), device="cuda")
+    cu, w = torch.zeros(3, dtype=torch.int32), torch.ones(64, device="cuda")
+    nsa.nsa_full_prefill(q, kv, kv, cu, h, q)
+    nsa.nsa_full_prefill_backward(q, kv, kv, q, lse, q, cu, h, q, kv, kv, None)
+    pos = torch.empty(0, dtype=torch.int32, device="cuda")
+    nsa.nsa_qk_norm_rope(q, kv, w, w, None, pos, h, rp, q, empty(3, 2, 64), kv, empty(3, 2, 64))
+    st = torch.cuda.Stream()
+    dw = [torch.full((64,), 5.0, device="cuda") for _ in range(2)]
+    st.wait_stream(torch.cuda.current_stream())
+    nsa.nsa_qk_norm_rope_backward(q, kv, w, w, None, pos, q, kv, h, rp, q, kv, *dw, None, stream=st)
+    st.synchronize()
+    assert (dw[0] == 0).all() and (dw[1] == 0).all()
