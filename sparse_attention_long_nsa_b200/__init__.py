@@ -442,7 +442,7 @@ def _bad(t, dtype, dev: int, name: str):
 
 def _in(t, dtype, dev: int, shape, name: str):
     """Device pointer of a contiguous tensor of that type, device and shape."""
-    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
         _bad(t, dtype, dev, name)
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -451,7 +451,7 @@ def _in(t, dtype, dev: int, shape, name: str):
 
 def _in_rows(t, dtype, dev: int, n: int, row, name: str):
     """Likewise of at least n rows of shape `row`."""
-    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
         _bad(t, dtype, dev, name)
     if t.shape[0] < n or t.shape[1:] != row:
         raise ValueError(f"{name}: expected [>= {n}, {', '.join(map(str, row))}], got {tuple(t.shape)}")
@@ -461,7 +461,7 @@ def _in_rows(t, dtype, dev: int, n: int, row, name: str):
 def _rows(t, n: int, heads: int, dim: int, dev: int, name: str) -> tuple:
     """(pointer, row stride) of bf16 rows [n, heads, dim] whose heads are packed: a
     whole tensor or a view of a fused projection."""
-    if t.dtype is not _BF16 or t.get_device() != dev:
+    if not isinstance(t, _Tensor) or t.dtype is not _BF16 or t.get_device() != dev:
         _bad(t, _BF16, dev, name)
     if t.shape != (n, heads, dim):
         raise ValueError(f"{name}: expected shape {(n, heads, dim)}, got {tuple(t.shape)}")
@@ -471,10 +471,18 @@ def _rows(t, n: int, heads: int, dim: int, dev: int, name: str) -> tuple:
     return t.data_ptr(), s0 if n > 1 else heads * dim   # one row: its stride means nothing
 
 
-_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_Tensor, _BF16, _F32, _I32, _I64 = torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.int64
+
+
+def _shape(t, name: str):
+    if not isinstance(t, _Tensor):
+        _bad(t, None, 0, name)
+    return t.shape
 
 
 def _device_of(t, name: str) -> int:
+    if not isinstance(t, _Tensor):
+        _bad(t, None, 0, name)
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name}: expected a CUDA tensor")
@@ -503,6 +511,8 @@ def _ws(ws, dev: int, n: int = 1):
         if n <= 0:
             return None, 0
         raise ValueError("ws: a workspace is needed (alloc_workspace of nsa_full_workspace_size bytes)")
+    if not isinstance(ws, _Tensor):
+        _bad(ws, None, dev, "ws")
     if ws.get_device() != dev or not ws.is_contiguous():
         _bad(ws, ws.dtype, dev, "ws")
     return ws.data_ptr(), ws.numel() * ws.element_size()
@@ -524,7 +534,7 @@ def nsa_qk_norm_rope(q, k, w_q, w_k, inv_freq, positions, heads: Heads, rope: Ro
     dev, N = _device_of(q, "q"), q.shape[0]
     qp, qs = _rows(q, N, Hq, dk, dev, "q")
     kp, ks = _rows(k, N, Hk, dk, dev, "k")
-    if k_out.shape[-2:] != (Hk, dk):
+    if _shape(k_out, "k_out")[-2:] != (Hk, dk):
         raise ValueError(f"k_out: expected [..., {Hk}, {dk}], got {tuple(k_out.shape)}")
     n_rows = k_out.numel() // (Hk * dk)
     if (v is None) != (v_out is None):
@@ -532,7 +542,7 @@ def nsa_qk_norm_rope(q, k, w_q, w_k, inv_freq, positions, heads: Heads, rope: Ro
     vp = vs = vo = None
     if v is not None:
         vp, vs = _rows(v, N, Hk, dv, dev, "v")
-        if v_out.shape[-2:] != (Hk, dv) or v_out.numel() != n_rows * Hk * dv:
+        if _shape(v_out, "v_out")[-2:] != (Hk, dv) or v_out.numel() != n_rows * Hk * dv:
             raise ValueError(f"v_out: expected [..., {Hk}, {dv}] with the rows of k_out, got {tuple(v_out.shape)}")
         vo = _in(v_out, _BF16, dev, v_out.shape, "v_out")
     args = (qp, qs, kp, ks, vp, vs or 0, _in(w_q, _F32, dev, (dk,), "w_q"), _in(w_k, _F32, dev, (dk,), "w_k"),
@@ -566,6 +576,8 @@ def nsa_qk_norm_rope_backward(q, k, w_q, w_k, inv_freq, positions, dq_out, dk_ou
 
 def _batch_of(cu_seqlens) -> tuple:
     """(pointer, batch, rows) of host int32 cu_seqlens."""
+    if not isinstance(cu_seqlens, _Tensor):
+        _bad(cu_seqlens, None, 0, "cu_seqlens")
     if cu_seqlens.dtype is not _I32 or cu_seqlens.is_cuda or not cu_seqlens.is_contiguous() or cu_seqlens.dim() != 1:
         raise ValueError("cu_seqlens: expected a host int32 tensor [batch + 1]")
     B = cu_seqlens.shape[0] - 1
@@ -612,7 +624,7 @@ def nsa_full_tree_decode(q, k_cache, v_cache, cache_lens, n_nodes, tree_mask, ma
     j (None: a chain)."""
     Hq, Hk, dk, dv = heads.H_q, heads.H_kv, heads.d_k, heads.d_v
     dev = _device_of(q, "q")
-    B, M, Lmax = q.shape[0], q.shape[1], k_cache.shape[1]
+    B, M, Lmax = q.shape[0], q.shape[1], _shape(k_cache, "k_cache")[1]
     _launch(dev, "nsa_full_tree_decode", lib().nsa_full_tree_decode, _in(q, _BF16, dev, (B, M, Hq, dk), "q"),
             _in(k_cache, _BF16, dev, (B, Lmax, Hk, dk), "k_cache"),
             _in(v_cache, _BF16, dev, (B, Lmax, Hk, dv), "v_cache"), _in(cache_lens, _I32, dev, (B,), "cache_lens"),
@@ -629,7 +641,7 @@ def nsa_full_tree_decode_paged(q, k_pool, v_pool, block_table, cache_lens, n_nod
     block_table [B, max_pages]."""
     Hq, Hk, dk, dv = heads.H_q, heads.H_kv, heads.d_k, heads.d_v
     dev = _device_of(q, "q")
-    B, M, pages, size, cols = q.shape[0], q.shape[1], k_pool.shape[0], k_pool.shape[1], block_table.shape[-1]
+    B, M, (pages, size), cols = q.shape[0], q.shape[1], _shape(k_pool, "k_pool")[:2], _shape(block_table, "block_table")[-1]
     _launch(dev, "nsa_full_tree_decode_paged", lib().nsa_full_tree_decode_paged,
             _in(q, _BF16, dev, (B, M, Hq, dk), "q"), _in(k_pool, _BF16, dev, (pages, size, Hk, dk), "k_pool"),
             _in(v_pool, _BF16, dev, (pages, size, Hk, dv), "v_pool"), pages, size,

@@ -3,6 +3,7 @@ import ctypes
 import os
 
 import pytest
+import torch
 
 import sparse_attention_long_nsa_b200 as nsa
 
@@ -52,3 +53,15 @@ def test_attention_over_empty_prompts_takes_null_arrays(L, back):
     for cu in ((0, 5, 0), (1, 1), (0, -1), (0, -4, 0), (0, 0, 3)):
         assert call(cu) == INV, cu
     assert call((0, 0), scale=-1.0) == INV and call((0, 0), h=nsa.Heads(64, 3, 192, 128)) == INV
+
+
+def test_binding_names_a_missing_first_tensor(L):
+    cu = torch.tensor([0, 3], dtype=torch.int32)
+    with pytest.raises(TypeError, match="^q: expected a tensor, got NoneType"):
+        nsa.nsa_full_prefill(None, None, None, cu, H, None)
+    with pytest.raises(TypeError, match="^cu_seqlens: expected a tensor, got list"):
+        nsa.nsa_full_prefill(None, None, None, [0, 3], H, None)
+    with pytest.raises(TypeError, match="^q: "):
+        nsa.nsa_qk_norm_rope(None, None, None, None, None, None, H, nsa.RopeParams(0, 0, 1e-6), None, None)
+    with pytest.raises(TypeError, match="^q: "):
+        nsa.nsa_full_tree_decode(None, None, None, None, None, None, 3, H, None)

@@ -149,3 +149,31 @@ def test_empty_calls_need_no_workspace():
     nsa.nsa_qk_norm_rope_backward(q, kv, w, w, None, pos, q, kv, h, rp, q, kv, *dw, None, stream=st)
     st.synchronize()
     assert (dw[0] == 0).all() and (dw[1] == 0).all()
+
+
+def test_binding_names_a_missing_tensor():
+    """None for a tensor that a call needs is a TypeError with the argument's name."""
+    h, rp = nsa.Heads(8, 2, 64, 64), nsa.RopeParams(32, 0, 1e-6)
+    q, kv, lse, w = empty(4, 8, 64), empty(4, 2, 64), torch.empty((4, 8), device="cuda"), torch.ones(64, device="cuda")
+    f, i32 = torch.ones(16, device="cuda"), torch.ones(4, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    ws = ws_for(nsa.NSA_OP_FULL_BACKWARD, h, 1, 4, 4)
+    q4, pool = q.unsqueeze(1), empty(4, 64, 2, 64)
+    calls = (
+        (nsa.nsa_qk_norm_rope, dict(q=q, k=kv, w_q=w, w_k=w, inv_freq=f, positions=i32, heads=h, rope=rp, q_out=q, k_out=kv), ()),
+        (nsa.nsa_qk_norm_rope_backward, dict(q=q, k=kv, w_q=w, w_k=w, inv_freq=f, positions=i32, dq_out=q, dk_out=kv, heads=h,
+                                             rope=rp, dq=q, dk=kv, dw_q=w, dw_k=w, ws=ws), ("ws",)),
+        (nsa.nsa_full_prefill, dict(q=q, k=kv, v=kv, cu_seqlens=cu, heads=h, out=q, ws=ws), ("ws",)),
+        (nsa.nsa_full_prefill_backward, dict(q=q, k=kv, v=kv, out=q, lse=lse, dout=q, cu_seqlens=cu, heads=h, dq=q, dk=kv, dv=kv,
+                                             ws=ws), ("ws",)),
+        (nsa.nsa_full_tree_decode, dict(q=q4, k_cache=pool, v_cache=pool, cache_lens=i32, n_nodes=None, tree_mask=None, max_len=64,
+                                        heads=h, out=q4, ws=ws), ("ws",)),
+        (nsa.nsa_full_tree_decode_paged, dict(q=q4, k_pool=pool, v_pool=pool, block_table=i32.view(4, 1), cache_lens=i32,
+                                              n_nodes=None, tree_mask=None, max_len=64, heads=h, out=q4, ws=ws), ("ws",)))
+    for fn, args, by_value in calls:
+        for name, t in args.items():
+            if isinstance(t, torch.Tensor):
+                with pytest.raises(ValueError if name in by_value else TypeError, match=rf"^{name}\b"):
+                    fn(**{**args, name: None})
+    with pytest.raises(TypeError, match="v_out"):
+        nsa.nsa_qk_norm_rope(q, kv, w, w, f, i32, h, rp, q, kv, kv, [1])
