@@ -420,7 +420,7 @@ typedef struct {
  *             differ. Rows that no token names are left as they were.
  *             A paged cache's row is page * page_size + offset.
  *   n_rows    rows of k_out and v_out (>= N when cache_rows is NULL)
- *   q_out     bf16 out [N, H_q, d_k]; may be q when q is packed
+ *   q_out     bf16 out [N, H_q, d_k]; may be q when q is packed (else refused)
  *   k_out     bf16 out [n_rows, H_kv, d_k]; may be k when packed and cache_rows is NULL
  *   v_out     bf16 out [n_rows, H_kv, d_v] or NULL
  * N = 0 launches nothing, and the arrays of tokens and rows may be NULL. No workspace. */
@@ -436,7 +436,7 @@ nsa_status_t nsa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, in
  *             gradients of q, k
  *   dw_q, dw_k fp32 out [d_k]: summed over tokens and heads in a fixed order (zeros
  *             for N = 0, where the arrays of tokens and the workspace may be NULL)
- * dq may be dq_out and dk may be dk_out (packed). Workspace:
+ * dq may be dq_out and dk may be dk_out (packed, else refused). Workspace:
  * nsa_full_workspace_size(NSA_OP_ROPE_BACKWARD, heads, 1, N, 0, 0). */
 nsa_status_t nsa_qk_norm_rope_backward(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                        const float* w_q, const float* w_k, const float* inv_freq,

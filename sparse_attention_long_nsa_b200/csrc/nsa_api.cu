@@ -1169,6 +1169,10 @@ nsa_status_t check_rope(const nsa_heads_t* heads, const nsa_rope_params_t* rope)
 
 // rows of `width` packed elements at a stride: not overlapping, aligned within the array
 bool stride_ok(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0; }
+// packed rows over rows of a stride: one array for both only when they coincide
+bool in_place_ok(const void* packed, const void* rows, int64_t stride, int64_t width, int64_t N) {
+  return packed != rows || stride == width || N == 1;
+}
 // an array that is read or written in 16-byte units
 bool array_ok(const void* p) { return p && aligned16(p); }
 
@@ -1257,6 +1261,9 @@ nsa_status_t nsa_qk_norm_rope(const void* q, int64_t q_stride, const void* k, in
   if (!array_ok(q) || !array_ok(k) || !positions || !array_ok(q_out) || !array_ok(k_out) || !aligned16(v) ||
       !aligned16(v_out) || !aligned_to(positions, 4) || !aligned_to(cache_rows, 8))
     return NSA_ERR_INVALID_ARG;
+  if (!in_place_ok(q_out, q, q_stride, (int64_t)heads->H_q * heads->d_k, N) ||
+      !in_place_ok(k_out, k, k_stride, (int64_t)heads->H_kv * heads->d_k, N))
+    return NSA_ERR_INVALID_ARG;
   RopeArgs a{};
   a.q = q; a.k = k; a.v = v;
   a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
@@ -1297,6 +1304,7 @@ nsa_status_t nsa_qk_norm_rope_backward(const void* q, int64_t q_stride, const vo
   if (!array_ok(q) || !array_ok(k) || !positions || !array_ok(dq_out) || !array_ok(dk_out) || !array_ok(dq) ||
       !array_ok(dk) || !array_ok(workspace) || !aligned_to(positions, 4))
     return NSA_ERR_INVALID_ARG;
+  if (!in_place_ok(dq_out, dq, dq_stride, wq, N) || !in_place_ok(dk_out, dk, dk_stride, wk, N)) return NSA_ERR_INVALID_ARG;
   if (ws_bytes < 256 + align256((size_t)kRopeBwdBlocks * 2 * heads->d_k * 4)) return NSA_ERR_WORKSPACE;
   RopeBwdArgs b{};
   RopeArgs& a = b.f;

@@ -65,3 +65,21 @@ def test_binding_names_a_missing_first_tensor(L):
         nsa.nsa_qk_norm_rope(None, None, None, None, None, None, H, nsa.RopeParams(0, 0, 1e-6), None, None)
     with pytest.raises(TypeError, match="^q: "):
         nsa.nsa_full_tree_decode(None, None, None, None, None, None, 3, H, None)
+
+
+# ---------------------------------------------------------------- in place
+
+def test_norm_in_place_needs_packed_rows(L):
+    """Outputs are packed: over inputs of a wider stride one token's result would lie
+    over another's input. One token, or packed rows, is allowed (and launches: not here)."""
+    h, rp = nsa.Heads(4, 1, 64, 64), nsa.RopeParams(64, 0, 1e-6)
+    A, B, C = 1 << 12, 1 << 13, 1 << 14      # addresses that no refused call follows
+
+    def forward(q_out=B, k_out=C, qs=256, ks=64, rows=None):
+        return L.nsa_qk_norm_rope(A, qs, A + 512, ks, None, 0, A, A, A, A, rows, 10, 10, ref(h), ref(rp), q_out, k_out, None, None)
+
+    def backward(dq=B, dk=C, dqs=256, dks=64):
+        return L.nsa_qk_norm_rope_backward(A, 256, A, 64, A, A, A, A, 10, B, C, ref(h), ref(rp), dq, dqs, dk, dks, A, A, A, 1 << 30,
+                                           None)
+    assert forward(q_out=A, qs=384) == INV and forward(k_out=A + 512, ks=384) == INV
+    assert backward(dqs=384) == INV and backward(dks=384) == INV
