@@ -465,20 +465,19 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
           const int key0 = (kt0 + t) * kFaKeys, left = nkeys - key0;   // keys of this tile (may exceed 128)
           if (fresh && (TREE ? key0 + kFaKeys > pre : left < kFaKeys)) {   // clear the V rows no row sees
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {                   // 64 keys each; bit i of `dead`: key 64 h + i
+            for (int h = 0; h < 2; ++h) {                   // 64 keys each
               const int have = left - 64 * h;
               if (have <= 0) continue;                      // not loaded
-              uint64_t dead;
+              int first = have;                             // prompts: the rows from there on
+              uint64_t dead = 0;                            // trees: bit i for key 64 h + i
               if (TREE) {
                 const int j = key0 + 64 * h - pre;          // node of the first key
                 dead = j >= 64 ? ~0ull : j >= 0 ? ~(named >> j) : j > -64 ? ~named << -j : 0ull;
-              } else {
-                dead = have >= 64 ? 0ull : ~0ull << have;
+                first = dead ? __ffsll((long long)dead) - 1 : 64;
               }
-              if (dead == 0) continue;
               uint8_t* vs = ring + (VC == 2 ? (p + h) % NS * kFaSlot : p % NS * kFaSlot + h * 8192);
-              for (int k = (__ffsll((long long)dead) - 1) * 8 + lane; k < 64 * 8; k += 32) {
-                if (!(dead >> (k >> 3) & 1)) continue;
+              for (int k = first * 8 + lane; k < 64 * 8; k += 32) {
+                if (TREE && !(dead >> (k >> 3) & 1)) continue;
                 *reinterpret_cast<uint4*>(vs + k * 16) = make_uint4(0, 0, 0, 0);
                 if (VC == 2) *reinterpret_cast<uint4*>(vs + 8192 + k * 16) = make_uint4(0, 0, 0, 0);
               }
