@@ -657,7 +657,9 @@ def nsa_full_tree_decode_paged(q, k_pool, v_pool, block_table, cache_lens, n_nod
 def tree_mask_from_parents(parents: torch.Tensor) -> torch.Tensor:
     """The tree_mask of nsa_full_tree_decode from parents [B, M] (integer; parents[b, i]
     < i is the node that node i continues, -1: none): int64 [B, M] on the same device,
-    each node's ancestors and itself."""
+    each node's ancestors and itself. Made once per shape of tree: it launches a few small
+    operations per node and reads the parents' check back (so it cannot be captured); where
+    trees change from step to step, parents on the host and a copy of the words are cheaper."""
     B, M = parents.shape
     if M > NSA_MAX_NODES:
         raise ValueError(f"at most {NSA_MAX_NODES} nodes, got {M}")

@@ -25,9 +25,10 @@
 // it hid (without the look-ahead every tile waited for its whole chain).
 // bwd_q: S 128, dP 128, dQ 192, dS 64; the next tile's S is issued before dQ.
 //
-// Measured, 4096 tokens, 64 heads on 4 key heads, 192 / 128: bwd_kv 657 us (four of the
-// seven products, 1.05 PFLOP/s, tensor pipe 57 % active), bwd_q 570 us (three, 0.96
-// PFLOP/s, 50 %), bwd_row 25 us, the merge 12 us.
+// Measured, 4096 tokens, 64 heads on 4 key heads, 192 / 128, each kernel alone (single
+// launches under the profiler): bwd_kv 655 us (four of the seven products, 1.05 PFLOP/s,
+// tensor pipe 57 % active), bwd_q 570 us (three, 0.96 PFLOP/s, 50 %), bwd_row 24 us, the
+// merge 11 us.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -864,9 +865,9 @@ static cudaError_t launch_bwd_t(const FullBwdArgs& a, const FullBwdMaps& m, cuda
   if (e != cudaSuccess) return e;
   const int64_t threads = a.n_rows * (DV / 8), W = a.kv_prefix[a.batch];
   nsa_full_bwd_row_kernel<DV><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a);
-  // no run shorter than four row tiles: the merge of many parts costs more than the
-  // SMs save (1024 tokens, 4 heads of 64, a training step: 54 us with four, 69 with one,
-  // 57 with two, 60 with six)
+  // no more runs than give each about four row tiles (rounded up: 5 tiles are runs of two
+  // and three): the merge of many parts costs more than the SMs save (1024 tokens, 4 heads
+  // of 64, a training step: 54 us with four, 69 with one, 57 with two, 60 with six)
   const int64_t want = (W + 3) / 4;
   const int runs = want < kFullBlocks ? (int)want : kFullBlocks;
   const int grid = a.n_items < kFullBlocks ? (int)a.n_items : kFullBlocks;

@@ -34,10 +34,11 @@
 // the rows see stays: a value of it that is not finite reaches the others too. Every wait
 // is bounded; on a timeout the block stops, lets its copies and products land and leaves.
 //
-// Measured: 8192 tokens, 64 heads on 4 key heads, 192 / 128: 1.12 ms by itself (1.22
-// PFLOP/s of 1.62 measured, tensor pipe 63 % active), 1.25 ms in a loop under the power
-// cap. 32 x 16 nodes over 16384 keys: 292 us (tensor pipe 51 %, 4.9 TB/s); 16 single
-// tokens over 8K to 128K keys: 515 us (5.8 TB/s).
+// Measured, this kernel alone (single launches under the profiler): 8192 tokens, 64 heads
+// on 4 key heads, 192 / 128: 1.09 ms (1.26 PFLOP/s of 1.62 measured, tensor pipe 63 %
+// active); calls in a row, under the power cap, take 1.23 to 1.27 ms. 32 x 16 nodes over
+// 16384 keys: 293 us (tensor pipe 51 %, 4.6 TB/s); 16 single tokens over 8K to 128K keys:
+// 500 us (6.0 TB/s).
 #pragma once
 
 #include <limits.h>
@@ -124,9 +125,9 @@ struct PrefillSched {
   }
 };
 
-// Runs that W key tiles are cut into: one a block, none shorter than two tiles (8
-// sequences of 1000 tokens: 14.9 us with two, 18.6 with one, 18.8 with three; one of
-// 8192: 24.5, 27.7, 25.0).
+// Runs that W key tiles are cut into: one a block, and no more than give each about two
+// tiles (8 sequences of 1000 tokens: 14.9 us with two, 18.6 with one, 18.8 with three; one
+// of 8192: 24.5, 27.7, 25.0). The count is rounded up: 3 tiles are runs of one and two.
 constexpr int kMinRun = 2;
 __device__ __forceinline__ int64_t tree_runs(int64_t W) {
   return min((int64_t)gridDim.x, (W + kMinRun - 1) / kMinRun);
@@ -161,6 +162,10 @@ struct TreeSched {
     const int cnt = min(ntile - s.kt0, end - pos);
     s.nkeys = L;
     s.nt[0] = cnt;
+    // A block of at most 128 rows in the 256-row kernel (few nodes in a call made for many)
+    // has one buffer at work: its scores, softmax and product with V take turns. Of 32
+    // sequences with up to 16 nodes of 16 heads half are such blocks, and the calls reach
+    // 0.55 of their memory floor.
     s.nt[1] = (NT == 2 && s.ntok > TOK / 2) ? cnt : 0;
     s.prefix = L - n;
     s.q_row = (int64_t)b * a.M + s.i0;
@@ -361,8 +366,9 @@ __global__ void __launch_bounds__(kFaThreads, 1) nsa_full_attn_kernel(const Full
         }
       };
       // A cache comes from memory: beside 256 rows of Q the ring does not cover its latency,
-      // and the tile after the next is asked into L2 (16 nodes over 16K: 359 -> 339 us;
-      // with 128 rows the ring is deeper and it costs 1%, two tiles ahead cost 5%).
+      // and the tile after the next is asked into L2 (32 x 16 nodes over 16K, calls in a
+      // row: 397 -> 356 us; with 128 rows the ring is deeper and it costs 1%, two tiles
+      // ahead cost 5%).
       auto prefetch = [&](int t) {
         int r0, r1;
         rows_of(t, r0, r1, blk2, brow2);

@@ -21,8 +21,8 @@
 // takes one token and four heads at a time: it forms the token's sines and cosines
 // (and, forward, their products with the weights) once, in registers, for all of its
 // heads; formed per head their loads and the index arithmetic bound the kernel.
-// 8192 tokens of 64 + 4 heads of 192: forward 90 us (4.7 TB/s of 6.55 measured),
-// backward 144 us (4.5 TB/s).
+// 8192 tokens of 64 + 4 heads of 192, calls in a row: forward 90 us (4.7 TB/s of 6.55
+// measured), backward 142 us (4.5 TB/s).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -263,7 +263,8 @@ __global__ void __launch_bounds__(kThreads, 2) nsa_qk_norm_rope_kernel(const Rop
 // and the key weight's (few heads) in shared memory of its own. part[block]: this
 // block's dw_q and dw_k, its lanes summed in a fixed order. At d_k = 192 a thread takes
 // 196 registers, one block an SM: held to two blocks it spilled, 177 us for 8K tokens
-// against 143.
+// against 143. The narrower heads keep that setting though they would fit twice (8K tokens
+// of 32 + 4 heads: 56 us at d_k = 64 and 67 at 128; two blocks an SM 41 and 54).
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kThreads, 1) nsa_qk_norm_rope_bwd_kernel(const RopeBwdArgs b) {
   constexpr int U = D / 64;
